@@ -74,6 +74,10 @@ extern "C" {
 #define NVFP4_ERROR_ARCH 5              /* current device is not gfx950 */
 #define NVFP4_ERROR_PRECONDITION 6      /* checked build only: see below */
 
+/* Element types of the calls that take more than one. */
+#define NVFP4_TYPE_F32 0
+#define NVFP4_TYPE_BF16 1
+
 /* Library version, major * 10000 + minor * 100 + patch. */
 int nvfp4_version(void);
 
@@ -386,6 +390,177 @@ int nvfp4_grouped_gemm_swiglu(const uint8_t* a_q, const uint8_t* a_sb, const flo
                               const int32_t* offsets, int64_t groups, const uint8_t* b_q,
                               const uint8_t* b_sb, const float* b_s, int64_t f, int64_t k,
                               uint16_t* h, float* amax, void* stream);
+
+/*
+ * bf16 products grouped by expert over the contiguous per-expert layout:
+ * the forward product of layers kept in bf16, and the two gradients of a
+ * grouped product, whose operands in the dequantized backward mode are what
+ * nvfp4_dequantize_rows writes.
+ *
+ * Defined by: the Miles page, section 反量化反向模式 (the dequantized backward
+ * runs its GEMMs in BF16 on the BF16 dequantization of the forward operands),
+ * and the miniTE page, section Transformer Engine路径优化 (contiguous layouts
+ * and device-side metadata).
+ *
+ *   nvfp4_bf16_grouped_gemm    Y[i]  = X[r(i)] W_e^T    y [m_total, n]
+ *   nvfp4_bf16_grouped_dgrad   dX[i] = dY[i] W_e        dx [m_total, k]
+ *   nvfp4_bf16_grouped_wgrad   dW_e  = add_e + sum over expert e's rows i of
+ *                              dY[i]^T X[r(i)]          dw [groups, n, k]
+ *
+ *   offsets   [groups+1] i32 device: expert e owns rows [offsets[e],
+ *             offsets[e+1]).  Non-decreasing; values are clamped to [0,
+ *             m_total].  Rows of y and dx that no expert owns are not
+ *             written, and such rows of dy and x are not read into any
+ *             result, whatever they hold; an expert without rows gets dw = 0
+ *             (or add).
+ *   x         [a_rows, k] bf16; row_index NULL: r(i) = i (a_rows >= m_total),
+ *             else [m_total] i32 device, indices outside [0, a_rows) stand
+ *             for rows of zeros.
+ *   w         [groups, n, k] bf16;  dy [m_total, n] bf16.
+ *   add       NULL or [groups, n, k] of dw's type; may be dw itself
+ *             (gradients added up in place).
+ *   *_type    NVFP4_TYPE_F32 or NVFP4_TYPE_BF16 of y, dx or dw.
+ * Products are exact and summed in fp32; a bf16 output is rounded once, to
+ * nearest even.  Infinities and NaN travel as in IEEE arithmetic.
+ * Deterministic: no atomics, and equal calls give equal bits.
+ * n % 8 == 0 and k % 8 == 0; n, k <= 2^20; groups <= 1024; a gathered x has
+ * fewer than 2^31 bytes.  n or k == 0 in the summed dimension gives zeros.
+ * The sum of a dX over a token's experts is nvfp4_moe_combine without
+ * weights.
+ * Errors: INVALID_VALUE (groups < 1, negative sizes, a type that is none,
+ * null pointers with work, a_rows < m_total without row_index),
+ * UNSUPPORTED_SHAPE (the limits above, tile grids past 2^28), MISALIGNED
+ * (operands and outputs 16 bytes, offsets and row_index 4), ARCH, LAUNCH.
+ */
+int nvfp4_bf16_grouped_gemm(const uint16_t* x, int64_t a_rows, const int32_t* row_index,
+                            int64_t m_total, const int32_t* offsets, int64_t groups,
+                            const uint16_t* w, int64_t n, int64_t k, void* y, int y_type,
+                            void* stream);
+int nvfp4_bf16_grouped_dgrad(const uint16_t* dy, int64_t m_total, const int32_t* offsets,
+                             int64_t groups, const uint16_t* w, int64_t n, int64_t k, void* dx,
+                             int dx_type, void* stream);
+int nvfp4_bf16_grouped_wgrad(const uint16_t* dy, int64_t m_total, const uint16_t* x, int64_t a_rows,
+                             const int32_t* row_index, const int32_t* offsets, int64_t groups,
+                             int64_t n, int64_t k, const void* add, void* dw, int dw_type,
+                             void* stream);
+
+/*
+ * The norms after and before a block, fused with the block's gate, the
+ * residual sum and the per-token NVFP4 quantization of the normed rows.
+ *
+ *   n  = b / sqrt(mean(b^2) + eps) * post_weight      (n = b without it)
+ *   r' = residual + scale * gate * n                  (rounded to its type)
+ *   h  = bf16(r' / sqrt(mean(r'^2) + eps) * norm_weight)
+ *
+ * Defined by: the miniTE page, section Transformer Engine路径优化 (amax reuse
+ * and fusion around the low-precision GEMMs): the rows that are quantized
+ * come out of a norm, as those of nvfp4_swiglu_quantize_rows out of SwiGLU.
+ *
+ *   x         [rows, d] block output b (fp32 as the GEMMs write it, or bf16).
+ *   residual  NULL (zeros) or [rows, d]; residual_out NULL or [rows, d] of
+ *             the same residual_type, may be residual itself.
+ *   post_weight, norm_weight  NULL or [d];  gate NULL, [d], or (gate_rows
+ *             nonzero) [rows, d]; all of param_type.
+ *   h NULL or [rows, d] bf16;  amax NULL or [rows] f32: max |h|;  q, sb, s
+ *             all NULL or all given: the bits of nvfp4_quantize_rows(h).
+ *             Any of them needs norm_weight.
+ * The norm before the next block sees the rounded r', so its backward pass
+ * from the stored r' is exact.  Sums of squares are held in fp32: values
+ * whose row of squares overflows fp32 normalize to zero.  eps >= 0; a row of
+ * zeros with eps == 0 is NaN, as the formula is.  Each row depends only on
+ * its own row.  d <= 16384; q, sb, s need d % 16 == 0.
+ *
+ * Backward, from dh (NULL: no gradient through h) and d_residual_out (NULL:
+ * zeros), at least one of them, with x and the stored residual_out r':
+ *   t = d_residual_out + (gradient of h through its norm);  d_residual = t
+ *   dx = gradient of b;  d_post_weight, d_norm_weight [d] f32;  d_gate [d]
+ *   f32, or (gate_rows) [rows, d] of param_type.  Any of d_residual,
+ *   d_post_weight, d_gate, d_norm_weight may be NULL.
+ *   d_residual_out and d_residual have residual_type and may be one buffer.
+ *   Column sums are added in a fixed order (no atomics).  workspace: at least
+ *   nvfp4_residual_norm_backward_workspace(rows, d) bytes of the caller's,
+ *   16-byte aligned, free for other use when the call's work has completed;
+ *   needed when one of the [d] gradients is asked for.  rows == 0 gives zero
+ *   column sums.
+ * Errors: INVALID_VALUE (sizes, types, eps, a missing or too small workspace,
+ * outputs without their inputs), UNSUPPORTED_SHAPE, MISALIGNED (elements to
+ * their size; with q, sb, s every tensor to 16 bytes), ARCH, LAUNCH.
+ */
+int nvfp4_residual_norm(const void* x, int x_type, const void* residual, int residual_type,
+                        const void* post_weight, const void* gate, int gate_rows,
+                        const void* norm_weight, int param_type, int64_t rows, int64_t d,
+                        float scale, float eps, void* residual_out, uint16_t* h, float* amax,
+                        uint8_t* q, uint8_t* sb, float* s, void* stream);
+int64_t nvfp4_residual_norm_backward_workspace(int64_t rows, int64_t d);
+int nvfp4_residual_norm_backward(const void* x, int x_type, const void* residual_out,
+                                 int residual_type, const void* post_weight, const void* gate,
+                                 int gate_rows, const void* norm_weight, int param_type,
+                                 const uint16_t* dh, const void* d_residual_out, int64_t rows,
+                                 int64_t d, float scale, float eps, void* dx, int dx_type,
+                                 void* d_residual, float* d_post_weight, void* d_gate,
+                                 float* d_norm_weight, void* workspace, int64_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * A token's sum over its experts' rows, and its gradient, through the layout
+ * nvfp4_moe_route writes.
+ *
+ *   out[t] = sum_j weights[t, j] * y[slot_of[t, j]]
+ *   dy[slot_of[t, j]] = weights[t, j] * dout[t]
+ *   d_weights[t, j]   = <dout[t], y[slot_of[t, j]]>
+ *
+ * Defined by: the miniTE page, section Transformer Engine路径优化 (contiguous
+ * layouts: the routed rows of the grouped GEMMs go back to their tokens).
+ *
+ *   y [y_rows, d], dout / out [tokens, d], dy [y_rows, d]: fp32 or bf16 each.
+ *   slot_of [tokens, topk] i32: a slot outside [0, y_rows) adds nothing and
+ *   gets no gradient (d_weights 0).  weights NULL (ones) or [tokens, topk]
+ *   f32.  dy and d_weights: either may be NULL, y too without d_weights.
+ * Forward: a row may be named by many slots.  Backward: no row may be named
+ * twice in one call (as in a routing's slot_of); its dy is then that of one
+ * of them.  Rows of dy that no slot names are not written.  Sums in fp32, in
+ * order j (dot products in a fixed order).  1 <= topk <= 64, d <= 2^24,
+ * tokens * topk <= 2^31.
+ * Errors: INVALID_VALUE, UNSUPPORTED_SHAPE, MISALIGNED (elements to their
+ * size), ARCH, LAUNCH.
+ */
+int nvfp4_moe_combine(const void* y, int y_type, int64_t y_rows, const int32_t* slot_of,
+                      const float* weights, int64_t tokens, int64_t topk, int64_t d, void* out,
+                      int out_type, void* stream);
+int nvfp4_moe_combine_backward(const void* dout, int dout_type, const void* y, int y_type,
+                               int64_t y_rows, const int32_t* slot_of, const float* weights,
+                               int64_t tokens, int64_t topk, int64_t d, void* dy, int dy_type,
+                               float* d_weights, void* stream);
+
+/*
+ * Global norm of many gradient tensors, and clipping by it.
+ *
+ *   norm = sqrt(sum over tensors of sum g^2)
+ *   out  = round(g * min(1, max_norm / (norm + 1e-6)))   in g's own type
+ *
+ * Defined by: the learner update of the TRIAGE page, section 核心方法; its
+ * gradients are what nvfp4_bf16_grouped_wgrad and the dense layers write.
+ *
+ *   grads, out, counts, types: HOST arrays of `tensors` entries, read during
+ *   the call (device pointers of the tensors, elements, NVFP4_TYPE_*); out
+ *   NULL: the norm only; out[i] may be grads[i], else the tensors must not
+ *   overlap (in place, no tensor may be listed twice).
+ *   norm NULL or [1] f32 device.  workspace: at least
+ *   nvfp4_clip_grad_norm_workspace(tensors) bytes of the caller's, 8-byte
+ *   aligned, free for other use when the call's work has completed.
+ * Squares are summed in fp64 (no overflow or underflow), in a fixed order;
+ * the norm is rounded once to fp32 and the factor once.  A NaN or infinite
+ * gradient gives a NaN or infinite norm and the formula's gradients.
+ * max_norm >= 0.  Addresses are part of a captured graph, as in every call.
+ * Errors: INVALID_VALUE (null arrays, negative counts, unknown types, neither
+ * out nor norm, a missing or too small workspace, max_norm < 0 or NaN),
+ * UNSUPPORTED_SHAPE (more than 2^20 tensors or 2^36 elements in one),
+ * MISALIGNED (elements to their size), ARCH, LAUNCH.
+ */
+int64_t nvfp4_clip_grad_norm_workspace(int64_t tensors);
+int nvfp4_clip_grad_norm(const void* const* grads, void* const* out, const int64_t* counts,
+                         const int32_t* types, int64_t tensors, float max_norm, float* norm,
+                         void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

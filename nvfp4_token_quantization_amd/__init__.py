@@ -14,6 +14,14 @@ Functions keep the C names:
   nvfp4_gemm(a, b)                                -> y
   nvfp4_grouped_gemm(a, offsets, b, row_index=None, m_total=None) -> y
   nvfp4_grouped_gemm_swiglu(a, offsets, b, row_index=None, m_total=None) -> (h, amax)
+  nvfp4_bf16_grouped_gemm(x, offsets, w, row_index=None)          -> y
+  nvfp4_bf16_grouped_dgrad(dy, offsets, w)                        -> dx
+  nvfp4_bf16_grouped_wgrad(dy, x, offsets, row_index=None, add=None) -> dw
+  nvfp4_residual_norm(x, residual, norm_weight, ...)              -> {"residual", "h", ...}
+  nvfp4_residual_norm_backward(x, residual, norm_weight, dh, d_residual, ...) -> {"dx", ...}
+  nvfp4_moe_combine(y, slot_of, weights=None)                     -> out
+  nvfp4_moe_combine_backward(dout, y, slot_of, weights=None)      -> {"dy", "d_weights"}
+  nvfp4_clip_grad_norm(grads, max_norm, out=None)                 -> norm
 
 (The codec self-test hooks live in the test-only ``selftest`` submodule over
 ``libnvfp4_selftest.so``.)
@@ -22,6 +30,7 @@ Layouts (all row-major): x bf16 [rows, k]; q uint8 [rows, k/2] with element
 2i in the low nibble; sb uint8 [rows, k/16] (E4M3 codes); s float32 [rows]
 (per-token) or [groups] (weights); a GEMM operand is the tuple (q, sb, s).
 """
+import bisect
 import ctypes
 import os
 
@@ -74,6 +83,25 @@ def load(path):
     L.nvfp4_mxfp8_quantize_rows.argtypes = [P, I64, I64, P, P, P]
     L.nvfp4_mxfp8_gemm.argtypes = [P, P, I64, P, P, I64, I64, P, P]
     L.nvfp4_mxfp8_grouped_gemm.argtypes = [P, P, I64, P, I64, P, I64, P, P, I64, I64, P, P]
+    I32, F32 = ctypes.c_int, ctypes.c_float
+    L.nvfp4_bf16_grouped_gemm.argtypes = [P, I64, P, I64, P, I64, P, I64, I64, P, I32, P]
+    L.nvfp4_bf16_grouped_dgrad.argtypes = [P, I64, P, I64, P, I64, I64, P, I32, P]
+    L.nvfp4_bf16_grouped_wgrad.argtypes = [P, I64, P, I64, P, P, I64, I64, I64, P, P, I32, P]
+    L.nvfp4_residual_norm.argtypes = [P, I32, P, I32, P, P, I32, P, I32, I64, I64, F32, F32,
+                                      P, P, P, P, P, P, P]
+    L.nvfp4_residual_norm_backward.argtypes = [P, I32, P, I32, P, P, I32, P, I32, P, P, I64, I64, F32,
+                                               F32, P, I32, P, P, P, P, P, I64, P]
+    L.nvfp4_moe_combine.argtypes = [P, I32, I64, P, P, I64, I64, I64, P, I32, P]
+    L.nvfp4_moe_combine_backward.argtypes = [P, I32, P, I32, I64, P, P, I64, I64, I64, P, I32, P, P]
+    L.nvfp4_clip_grad_norm.argtypes = [P, P, P, P, I64, F32, P, P, I64, P]
+    L.nvfp4_residual_norm_backward_workspace.argtypes = [I64, I64]
+    L.nvfp4_residual_norm_backward_workspace.restype = I64
+    L.nvfp4_clip_grad_norm_workspace.argtypes = [I64]
+    L.nvfp4_clip_grad_norm_workspace.restype = I64
+    for f in ("nvfp4_bf16_grouped_gemm", "nvfp4_bf16_grouped_dgrad", "nvfp4_bf16_grouped_wgrad",
+              "nvfp4_residual_norm", "nvfp4_residual_norm_backward", "nvfp4_moe_combine",
+              "nvfp4_moe_combine_backward", "nvfp4_clip_grad_norm"):
+        getattr(L, f).restype = ctypes.c_int
     for f in ("nvfp4_quantize_rows", "nvfp4_quantize_weight", "nvfp4_gemm",
               "nvfp4_swiglu_quantize_rows", "nvfp4_moe_route", "nvfp4_dequantize_rows",
               "nvfp4_mxfp8_quantize_rows", "nvfp4_mxfp8_gemm", "nvfp4_mxfp8_grouped_gemm",
@@ -502,3 +530,416 @@ def nvfp4_grouped_gemm_swiglu(a, offsets, b, row_index=None, m_total=None, out=N
                                          _ptr(bs), f, k, _ptr(h), _ptr(amax), _stream(dev))
     _check("nvfp4_grouped_gemm_swiglu", st)
     return h, amax
+
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}  # NVFP4_TYPE_*
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _type(t):
+    return 0 if t is None else _TYPES[t.dtype]
+
+
+def _out_dtype(dtype):
+    if dtype not in _TYPES:
+        raise TypeError("an output dtype is torch.float32 or torch.bfloat16 (got %s)" % dtype)
+    return dtype
+
+
+def _no_overlap(out, name, *inputs):
+    """An output that shares memory with an input would be read while it is written."""
+    if out is None or out.numel() == 0:
+        return
+    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for t in inputs:
+        if t is not None and t.numel() and t.data_ptr() < hi and lo < t.data_ptr() + t.numel() * t.element_size():
+            raise ValueError("%s must not overlap an input" % name)
+
+
+def _experts(offsets, groups, dev):
+    _dev(offsets, "offsets", (torch.int32,), 1)
+    if offsets.numel() != groups + 1:
+        raise ValueError("offsets must have groups + 1 entries")
+    _same_device(dev, ("offsets", offsets))
+
+
+def nvfp4_bf16_grouped_gemm(x, offsets, w, row_index=None, m_total=None, out=None, out_dtype=torch.float32):
+    """bf16 product grouped by expert: Y[i] = X[r(i)] W_e^T for the rows i of
+    expert e, r(i) = row_index[i] or i.
+
+    x bf16 [a_rows, k]; offsets int32 [groups+1] (device); w bf16 [groups, n,
+    k]; row_index optional int32 [m_total] (indices outside x are zero rows).
+    m_total as for nvfp4_grouped_gemm.  Returns [m_total, n] of out_dtype
+    (float32 or bfloat16); rows that no expert owns are not written.
+    n % 8 == 0, k % 8 == 0.
+    """
+    _dev(x, "x", (torch.bfloat16,), 2)
+    _dev(w, "w", (torch.bfloat16,), 3)
+    groups, n, k = w.shape
+    if x.shape[1] != k:
+        raise ValueError("x and w must have the same k")
+    dev = x.device
+    _experts(offsets, groups, dev)
+    m_total = _grouped_rows(x.shape[0], row_index, m_total)
+    _same_device(dev, ("w", w), ("row_index", row_index))
+    if out is None:
+        out = torch.empty((m_total, n), dtype=_out_dtype(out_dtype), device=dev)
+    else:
+        _out_rows(out, "out", m_total, n, _out_dtype(out.dtype), dev)
+        _no_overlap(out, "out", x, w, offsets, row_index)
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_bf16_grouped_gemm(_ptr(x), x.shape[0], _ptr(row_index), m_total, _ptr(offsets), groups,
+                                           _ptr(w), n, k, _ptr(out), _type(out), _stream(dev))
+    _check("nvfp4_bf16_grouped_gemm", st)
+    return out
+
+
+def nvfp4_bf16_grouped_dgrad(dy, offsets, w, m_total=None, out=None, out_dtype=torch.float32):
+    """Data gradient of the grouped product: dX[i] = dY[i] W_e for the rows i
+    of expert e.  dy bf16 [m_total, n], w bf16 [groups, n, k] (as
+    nvfp4_dequantize_rows writes it in the dequantized backward mode); returns
+    the routed rows' gradients [m_total, k] of out_dtype.  A token's own
+    gradient is their sum, nvfp4_moe_combine(dx, slot_of)."""
+    _dev(dy, "dy", (torch.bfloat16,), 2)
+    _dev(w, "w", (torch.bfloat16,), 3)
+    groups, n, k = w.shape
+    if dy.shape[1] != n:
+        raise ValueError("dy and w must have the same n")
+    dev = dy.device
+    _experts(offsets, groups, dev)
+    m_total = _grouped_rows(dy.shape[0], None, m_total)
+    _same_device(dev, ("w", w))
+    if out is None:
+        out = torch.empty((m_total, k), dtype=_out_dtype(out_dtype), device=dev)
+    else:
+        _out_rows(out, "out", m_total, k, _out_dtype(out.dtype), dev)
+        _no_overlap(out, "out", dy, w, offsets)
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_bf16_grouped_dgrad(_ptr(dy), m_total, _ptr(offsets), groups, _ptr(w), n, k, _ptr(out),
+                                            _type(out), _stream(dev))
+    _check("nvfp4_bf16_grouped_dgrad", st)
+    return out
+
+
+def nvfp4_bf16_grouped_wgrad(dy, x, offsets, row_index=None, add=None, out=None, out_dtype=torch.float32):
+    """Weight gradient of the grouped product: dW_e = add_e + the sum over
+    expert e's rows i of dY[i]^T X[r(i)].
+
+    dy bf16 [m_total, n]; x bf16 [a_rows, k]; row_index optional int32
+    [m_total]; add optional [groups, n, k] of the output's dtype, which may be
+    `out` itself (gradients of several microbatches added up in place).
+    Returns [groups, n, k]: zeros (or add) for an expert without rows.
+    """
+    _dev(dy, "dy", (torch.bfloat16,), 2)
+    _dev(x, "x", (torch.bfloat16,), 2)
+    _dev(offsets, "offsets", (torch.int32,), 1)
+    groups = offsets.numel() - 1
+    if groups < 1:
+        raise ValueError("offsets must have groups + 1 entries, groups >= 1")
+    m_total, n = dy.shape
+    k = x.shape[1]
+    dev = dy.device
+    _grouped_rows(x.shape[0], row_index, m_total)
+    _same_device(dev, ("x", x), ("offsets", offsets), ("row_index", row_index), ("add", add))
+    shape = (groups, n, k)
+    if add is not None:
+        _dev(add, "add", _FLOATS, 3)
+        if tuple(add.shape) != shape:
+            raise ValueError("add must have shape %s (got %s)" % (shape, tuple(add.shape)))
+    if out is None:
+        out = torch.empty(shape, dtype=_out_dtype(out_dtype) if add is None else add.dtype, device=dev)
+    else:
+        _out(out, "out", shape, _out_dtype(out.dtype), dev)
+        _no_overlap(out, "out", dy, x, offsets, row_index)
+    if add is not None:
+        if add.dtype != out.dtype:
+            raise TypeError("add must have the output's dtype %s (got %s)" % (out.dtype, add.dtype))
+        if add.data_ptr() != out.data_ptr():
+            _no_overlap(out, "out", add)
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_bf16_grouped_wgrad(_ptr(dy), m_total, _ptr(x), x.shape[0], _ptr(row_index), _ptr(offsets),
+                                            groups, n, k, _ptr(add), _ptr(out), _type(out), _stream(dev))
+    _check("nvfp4_bf16_grouped_wgrad", st)
+    return out
+
+
+def _norm_params(dev, rows, d, **params):
+    """Check the parameters of the residual norms (one dtype, [d]; the gate
+    [d] or [rows, d]); returns (param dtype, gate is per row)."""
+    dtype = None
+    for name, t in params.items():
+        if t is None:
+            continue
+        _dev(t, name, _FLOATS)
+        if tuple(t.shape) != (d,) and not (name == "gate" and tuple(t.shape) == (rows, d)):
+            raise ValueError("%s must have shape (%d,)%s (got %s)" % (
+                name, d, " or (%d, %d)" % (rows, d) if name == "gate" else "", tuple(t.shape)))
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError("post_weight, gate and norm_weight must have one dtype (got %s and %s)" % (dtype, t.dtype))
+        dtype = t.dtype
+        _same_device(dev, (name, t))
+    gate = params.get("gate")
+    return dtype or torch.float32, gate is not None and gate.dim() == 2
+
+
+def _like(t, name, ref, dtypes=None):
+    _dev(t, name, dtypes or (ref.dtype,), 2)
+    if t.shape != ref.shape:
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(ref.shape), tuple(t.shape)))
+    _same_device(ref.device, (name, t))
+
+
+def nvfp4_residual_norm(x, residual=None, norm_weight=None, post_weight=None, gate=None, scale=1.0, eps=1e-6,
+                        want_h=True, want_amax=False, quantize=False, residual_dtype=None, out=None):
+    """The norms after and before a block with its gate and residual:
+
+      n = x / sqrt(mean(x^2) + eps) * post_weight   (n = x without it)
+      r' = residual + scale * gate * n
+      h = r' / sqrt(mean(r'^2) + eps) * norm_weight, bf16
+
+    x [rows, d] float32 or bfloat16; residual [rows, d] (None: zeros, and r'
+    has residual_dtype, bfloat16 unless given); post_weight and norm_weight
+    [d], gate [d] or [rows, d], of one dtype.  Returns a dict: "residual" (r',
+    in the residual's dtype) and, with norm_weight, "h" (want_h), "amax"
+    (want_amax: float32 [rows], max |h|) and "q", "sb", "s" (quantize: as
+    nvfp4_quantize_rows(h)).  `out` may hold preallocated tensors under the
+    same keys; its "residual" may be `residual` itself.
+    """
+    _dev(x, "x", _FLOATS, 2)
+    rows, d = x.shape
+    dev = x.device
+    ptype, gate_rows = _norm_params(dev, rows, d, post_weight=post_weight, gate=gate, norm_weight=norm_weight)
+    if residual is not None:
+        _like(residual, "residual", x, _FLOATS)
+        if residual_dtype not in (None, residual.dtype):
+            raise TypeError("residual_dtype must be the residual's own dtype")
+        rdt = residual.dtype
+    else:
+        rdt = _out_dtype(residual_dtype or torch.bfloat16)
+    if norm_weight is None:
+        if want_amax or quantize:
+            raise ValueError("amax and the quantized rows need norm_weight")
+        want_h = False
+    want = [("residual", (rows, d), rdt)]
+    if want_h:
+        want.append(("h", (rows, d), torch.bfloat16))
+    if want_amax:
+        want.append(("amax", (rows,), torch.float32))
+    if quantize:
+        want += [("q", (rows, d // 2), torch.uint8), ("sb", (rows, d // 16), torch.uint8),
+                 ("s", (rows,), torch.float32)]
+    out = out or {}
+    res = {}
+    for key, shape, dt in want:
+        t = out.get(key)
+        if t is None:
+            res[key] = torch.empty(shape, dtype=dt, device=dev)
+            continue
+        res[key] = _out(t, "out " + key, shape, dt, dev)
+        same = key == "residual" and residual is not None and t.data_ptr() == residual.data_ptr()
+        _no_overlap(t, "out " + key, x, None if same else residual, post_weight, gate, norm_weight)
+    g = res.get
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_residual_norm(_ptr(x), _type(x), _ptr(residual), _TYPES[rdt], _ptr(post_weight), _ptr(gate),
+                                       int(gate_rows), _ptr(norm_weight), _TYPES[ptype], rows, d, float(scale),
+                                       float(eps), _ptr(res["residual"]), _ptr(g("h")), _ptr(g("amax")), _ptr(g("q")),
+                                       _ptr(g("sb")), _ptr(g("s")), _stream(dev))
+    _check("nvfp4_residual_norm", st)
+    return res
+
+
+def nvfp4_residual_norm_backward(x, residual, norm_weight=None, dh=None, d_residual=None, post_weight=None, gate=None,
+                                 scale=1.0, eps=1e-6, dx_dtype=torch.bfloat16, out=None, workspace=None):
+    """Backward pass of nvfp4_residual_norm.
+
+    x: the block output; residual: the stored new residual r' (not the one
+    that went in); dh bf16 [rows, d] and d_residual (residual's dtype), the
+    gradients of h and of r' (either may be None).  Returns a dict: "dx"
+    (dx_dtype), "d_residual" (gradient of the residual that went in), and for
+    the parameters given "d_post_weight", "d_norm_weight" (float32 [d]) and
+    "d_gate" (float32 [d], or [rows, d] of the gate's dtype).  `out` may hold
+    preallocated tensors under these keys; its "d_residual" may be
+    `d_residual` itself.  workspace: optional uint8 tensor of at least
+    nvfp4_residual_norm_backward_workspace(rows, d) bytes.
+    """
+    _dev(x, "x", _FLOATS, 2)
+    rows, d = x.shape
+    dev = x.device
+    ptype, gate_rows = _norm_params(dev, rows, d, post_weight=post_weight, gate=gate, norm_weight=norm_weight)
+    _like(residual, "residual", x, _FLOATS)
+    if dh is None and d_residual is None:
+        raise ValueError("dh or d_residual must be given")
+    if dh is not None:
+        if norm_weight is None:
+            raise ValueError("dh needs norm_weight")
+        _like(dh, "dh", x, (torch.bfloat16,))
+    if d_residual is not None:
+        _like(d_residual, "d_residual", residual)
+    want = [("dx", (rows, d), _out_dtype(dx_dtype)), ("d_residual", (rows, d), residual.dtype)]
+    if post_weight is not None:
+        want.append(("d_post_weight", (d,), torch.float32))
+    if gate is not None:
+        want.append(("d_gate", (rows, d), gate.dtype) if gate_rows else ("d_gate", (d,), torch.float32))
+    if norm_weight is not None:
+        want.append(("d_norm_weight", (d,), torch.float32))
+    out = out or {}
+    res = {}
+    for key, shape, dt in want:
+        t = out.get(key)
+        if t is None:
+            res[key] = torch.empty(shape, dtype=dt, device=dev)
+            continue
+        res[key] = _out(t, "out " + key, shape, dt, dev)
+        same = key == "d_residual" and d_residual is not None and t.data_ptr() == d_residual.data_ptr()
+        _no_overlap(t, "out " + key, x, residual, dh, None if same else d_residual, post_weight, gate, norm_weight)
+    g = res.get
+    need = lib().nvfp4_residual_norm_backward_workspace(rows, d)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    else:
+        _dev(workspace, "workspace", (torch.uint8,), 1)
+        _same_device(dev, ("workspace", workspace))
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_residual_norm_backward(
+            _ptr(x), _type(x), _ptr(residual), _type(residual), _ptr(post_weight), _ptr(gate), int(gate_rows),
+            _ptr(norm_weight), _TYPES[ptype], _ptr(dh), _ptr(d_residual), rows, d, float(scale), float(eps),
+            _ptr(res["dx"]), _TYPES[dx_dtype], _ptr(res["d_residual"]), _ptr(g("d_post_weight")), _ptr(g("d_gate")),
+            _ptr(g("d_norm_weight")), _ptr(workspace), workspace.numel(), _stream(dev))
+    _check("nvfp4_residual_norm_backward", st)
+    return res
+
+
+def _slots(slot_of, weights, dev):
+    _dev(slot_of, "slot_of", (torch.int32,), 2)
+    _same_device(dev, ("slot_of", slot_of), ("weights", weights))
+    if weights is not None:
+        _dev(weights, "weights", (torch.float32,), 2)
+        if weights.shape != slot_of.shape:
+            raise ValueError("weights must have slot_of's shape %s (got %s)" % (tuple(slot_of.shape),
+                                                                              tuple(weights.shape)))
+    return slot_of.shape
+
+
+def nvfp4_moe_combine(y, slot_of, weights=None, out=None, out_dtype=torch.bfloat16):
+    """A token's sum over its experts' rows: out[t] = sum_j weights[t, j] *
+    y[slot_of[t, j]].  y [rows, d] float32 or bfloat16; slot_of int32 [tokens,
+    topk] as nvfp4_moe_route writes it (a slot outside y adds nothing);
+    weights optional float32 [tokens, topk].  Returns [tokens, d]."""
+    _dev(y, "y", _FLOATS, 2)
+    dev = y.device
+    tokens, topk = _slots(slot_of, weights, dev)
+    d = y.shape[1]
+    if out is None:
+        out = torch.empty((tokens, d), dtype=_out_dtype(out_dtype), device=dev)
+    else:
+        _out(out, "out", (tokens, d), _out_dtype(out.dtype), dev)
+        _no_overlap(out, "out", y, slot_of, weights)
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_moe_combine(_ptr(y), _type(y), y.shape[0], _ptr(slot_of), _ptr(weights), tokens, topk, d,
+                                     _ptr(out), _type(out), _stream(dev))
+    _check("nvfp4_moe_combine", st)
+    return out
+
+
+def nvfp4_moe_combine_backward(dout, y, slot_of, weights=None, dy_dtype=torch.bfloat16, out=None):
+    """Backward pass of nvfp4_moe_combine: "dy" [rows, d] (dy[slot_of[t, j]] =
+    weights[t, j] * dout[t]; rows that no slot names are not written) and,
+    with weights, "d_weights" [tokens, topk].  No row may be named twice.
+    `out` may hold preallocated tensors under these keys."""
+    _dev(y, "y", _FLOATS, 2)
+    dev = y.device
+    tokens, topk = _slots(slot_of, weights, dev)
+    d = y.shape[1]
+    _dev(dout, "dout", _FLOATS, 2)
+    if tuple(dout.shape) != (tokens, d):
+        raise ValueError("dout must have shape (%d, %d) (got %s)" % (tokens, d, tuple(dout.shape)))
+    _same_device(dev, ("dout", dout))
+    out = out or {}
+    dy = out.get("dy")
+    if dy is None:
+        dy = torch.empty(tuple(y.shape), dtype=_out_dtype(dy_dtype), device=dev)
+    else:
+        _out(dy, "out dy", tuple(y.shape), _out_dtype(dy.dtype), dev)
+        _no_overlap(dy, "out dy", dout, y, slot_of, weights)
+    res = {"dy": dy}
+    if weights is not None:
+        dw = out.get("d_weights")
+        if dw is None:
+            dw = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
+        else:
+            _out(dw, "out d_weights", (tokens, topk), torch.float32, dev)
+            _no_overlap(dw, "out d_weights", dout, y, slot_of, weights)
+        res["d_weights"] = dw
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_moe_combine_backward(_ptr(dout), _type(dout), _ptr(y), _type(y), y.shape[0], _ptr(slot_of),
+                                              _ptr(weights), tokens, topk, d, _ptr(dy), _type(dy),
+                                              _ptr(res.get("d_weights")), _stream(dev))
+    _check("nvfp4_moe_combine_backward", st)
+    return res
+
+
+def nvfp4_clip_grad_norm(grads, max_norm, out=None, norm_only=False, workspace=None):
+    """Global norm of gradient tensors (float32 and bfloat16, any shapes, one
+    device) and clipping by it: g *= min(1, max_norm / (norm + 1e-6)).
+
+    Clips in place (no tensor may then be listed twice), into the tensors of
+    `out` (same shapes and dtypes) when given, or not at all with norm_only.
+    Returns the norm as a float32 scalar tensor on the device; the host never
+    waits.  workspace: optional uint8 tensor of at least
+    nvfp4_clip_grad_norm_workspace(len(grads)) bytes.
+    """
+    grads = list(grads)
+    n = len(grads)
+    if n == 0:
+        raise ValueError("grads must hold at least one tensor")
+    dev = grads[0].device
+    for i, t in enumerate(grads):
+        _dev(t, "grads[%d]" % i, _FLOATS)
+        if t.device != dev:
+            raise ValueError("grads[%d] must be on %s (got %s)" % (i, dev, t.device))
+    if norm_only:
+        if out is not None:
+            raise ValueError("norm_only takes no out")
+    elif out is None:
+        out = grads
+    else:
+        out = list(out)
+        if len(out) != n:
+            raise ValueError("out must have one tensor per gradient")
+        for i, (t, g) in enumerate(zip(out, grads)):
+            _out(t, "out[%d]" % i, tuple(g.shape), g.dtype, dev)
+    if out is not None:
+        _disjoint(grads, out)
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
+    outs = None if out is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
+    counts = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
+    types = (ctypes.c_int32 * n)(*[_TYPES[t.dtype] for t in grads])
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty((lib().nvfp4_clip_grad_norm_workspace(n),), dtype=torch.uint8, device=dev)
+    else:
+        _dev(workspace, "workspace", (torch.uint8,), 1)
+        _same_device(dev, ("workspace", workspace))
+    with torch.cuda.device(dev):
+        st = lib().nvfp4_clip_grad_norm(ptrs, outs, counts, types, n, float(max_norm), _ptr(norm), _ptr(workspace),
+                                        workspace.numel(), _stream(dev))
+    _check("nvfp4_clip_grad_norm", st)
+    return norm
+
+
+def _disjoint(grads, out):
+    """No output may share memory with another output or another gradient: it
+    would be read, or scaled twice, after it was written."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i)
+                   for i, t in enumerate(out) if t.numel())
+    for (_, end, _), (lo, _, i) in zip(spans, spans[1:]):
+        if lo < end:
+            raise ValueError("out tensors must not overlap (tensor %d)" % i)
+    if out is grads:
+        return
+    starts = [s[0] for s in spans]
+    for i, g in enumerate(grads):
+        lo, hi = g.data_ptr(), g.data_ptr() + g.numel() * g.element_size()
+        k = bisect.bisect_left(starts, hi) - 1  # the last output that starts below the gradient's end
+        if g.numel() and k >= 0 and spans[k][1] > lo and (spans[k][0] != lo or spans[k][2] != i):
+            raise ValueError("out must not overlap another gradient (tensor %d)" % i)
