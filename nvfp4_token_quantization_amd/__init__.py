@@ -31,6 +31,7 @@ Layouts (all row-major): x bf16 [rows, k]; q uint8 [rows, k/2] with element
 (per-token) or [groups] (weights); a GEMM operand is the tuple (q, sb, s).
 """
 import bisect
+import contextlib
 import ctypes
 import os
 
@@ -536,6 +537,15 @@ _TYPES = {torch.float32: 0, torch.bfloat16: 1}  # NVFP4_TYPE_*
 _FLOATS = (torch.float32, torch.bfloat16)
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(dev):
+    """The tensors' device as the current one for a call's launches (entering
+    it costs microseconds, so only where it is not current already)."""
+    return _HERE_ALREADY if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
 def _type(t):
     return 0 if t is None else _TYPES[t.dtype]
 
@@ -587,7 +597,7 @@ def nvfp4_bf16_grouped_gemm(x, offsets, w, row_index=None, m_total=None, out=Non
     else:
         _out_rows(out, "out", m_total, n, _out_dtype(out.dtype), dev)
         _no_overlap(out, "out", x, w, offsets, row_index)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().nvfp4_bf16_grouped_gemm(_ptr(x), x.shape[0], _ptr(row_index), m_total, _ptr(offsets), groups,
                                            _ptr(w), n, k, _ptr(out), _type(out), _stream(dev))
     _check("nvfp4_bf16_grouped_gemm", st)
@@ -614,7 +624,7 @@ def nvfp4_bf16_grouped_dgrad(dy, offsets, w, m_total=None, out=None, out_dtype=t
     else:
         _out_rows(out, "out", m_total, k, _out_dtype(out.dtype), dev)
         _no_overlap(out, "out", dy, w, offsets)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().nvfp4_bf16_grouped_dgrad(_ptr(dy), m_total, _ptr(offsets), groups, _ptr(w), n, k, _ptr(out),
                                             _type(out), _stream(dev))
     _check("nvfp4_bf16_grouped_dgrad", st)
@@ -656,7 +666,7 @@ def nvfp4_bf16_grouped_wgrad(dy, x, offsets, row_index=None, add=None, out=None,
             raise TypeError("add must have the output's dtype %s (got %s)" % (out.dtype, add.dtype))
         if add.data_ptr() != out.data_ptr():
             _no_overlap(out, "out", add)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().nvfp4_bf16_grouped_wgrad(_ptr(dy), m_total, _ptr(x), x.shape[0], _ptr(row_index), _ptr(offsets),
                                             groups, n, k, _ptr(add), _ptr(out), _type(out), _stream(dev))
     _check("nvfp4_bf16_grouped_wgrad", st)
@@ -739,7 +749,7 @@ def nvfp4_residual_norm(x, residual=None, norm_weight=None, post_weight=None, ga
         same = key == "residual" and residual is not None and t.data_ptr() == residual.data_ptr()
         _no_overlap(t, "out " + key, x, None if same else residual, post_weight, gate, norm_weight)
     g = res.get
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().nvfp4_residual_norm(_ptr(x), _type(x), _ptr(residual), _TYPES[rdt], _ptr(post_weight), _ptr(gate),
                                        int(gate_rows), _ptr(norm_weight), _TYPES[ptype], rows, d, float(scale),
                                        float(eps), _ptr(res["residual"]), _ptr(g("h")), _ptr(g("amax")), _ptr(g("q")),
@@ -799,7 +809,7 @@ def nvfp4_residual_norm_backward(x, residual, norm_weight=None, dh=None, d_resid
     else:
         _dev(workspace, "workspace", (torch.uint8,), 1)
         _same_device(dev, ("workspace", workspace))
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().nvfp4_residual_norm_backward(
             _ptr(x), _type(x), _ptr(residual), _type(residual), _ptr(post_weight), _ptr(gate), int(gate_rows),
             _ptr(norm_weight), _TYPES[ptype], _ptr(dh), _ptr(d_residual), rows, d, float(scale), float(eps),
@@ -834,7 +844,7 @@ def nvfp4_moe_combine(y, slot_of, weights=None, out=None, out_dtype=torch.bfloat
     else:
         _out(out, "out", (tokens, d), _out_dtype(out.dtype), dev)
         _no_overlap(out, "out", y, slot_of, weights)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().nvfp4_moe_combine(_ptr(y), _type(y), y.shape[0], _ptr(slot_of), _ptr(weights), tokens, topk, d,
                                      _ptr(out), _type(out), _stream(dev))
     _check("nvfp4_moe_combine", st)
@@ -870,7 +880,7 @@ def nvfp4_moe_combine_backward(dout, y, slot_of, weights=None, dy_dtype=torch.bf
             _out(dw, "out d_weights", (tokens, topk), torch.float32, dev)
             _no_overlap(dw, "out d_weights", dout, y, slot_of, weights)
         res["d_weights"] = dw
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().nvfp4_moe_combine_backward(_ptr(dout), _type(dout), _ptr(y), _type(y), y.shape[0], _ptr(slot_of),
                                               _ptr(weights), tokens, topk, d, _ptr(dy), _type(dy),
                                               _ptr(res.get("d_weights")), _stream(dev))
@@ -920,7 +930,7 @@ def nvfp4_clip_grad_norm(grads, max_norm, out=None, norm_only=False, workspace=N
     else:
         _dev(workspace, "workspace", (torch.uint8,), 1)
         _same_device(dev, ("workspace", workspace))
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib().nvfp4_clip_grad_norm(ptrs, outs, counts, types, n, float(max_norm), _ptr(norm), _ptr(workspace),
                                         workspace.numel(), _stream(dev))
     _check("nvfp4_clip_grad_norm", st)

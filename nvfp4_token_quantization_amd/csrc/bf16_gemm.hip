@@ -21,7 +21,6 @@ struct Bf16Args {
   const void* add;
   void* y;
   bool y_bf;
-  TileGrid t;
 };
 
 // ---------------------------------------------------------------------------
@@ -45,14 +44,16 @@ struct Bf16Args {
 //     lanes (and of 32) lie in different banks.
 // Rows, columns and summed elements that do not exist get an offset past the
 // resource, for which the DMA writes zeros.
-constexpr int BG_BK = 32;
-constexpr int BG_BUFS = 4;
 constexpr uint32_t BG_OOB = 0x80000000u;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ int bg_row_swz(int r) { return ((r >> 2) + (r & 2)) & 3; }
+// chunk swizzle of a row operand's LDS row of BK elements (4 or 8 chunks)
+template <int BK>
+__device__ __forceinline__ int bg_row_swz(int r) {
+  return BK == 64 ? (r >> 1) & 7 : ((r >> 2) + (r & 2)) & 3;
+}
 // chunk swizzle of a column operand's LDS row of 8 TN chunks
 template <int TN>
 __device__ __forceinline__ int bg_col_swz(int r) {
@@ -70,7 +71,7 @@ struct BgOperand {
   i32x4 rsrc;
   const uint8_t* base;   // column operands: of summed index 0
   int64_t stride;        // column operands: bytes per summed index
-  uint32_t voff[T];      // this lane's byte offset for its DMA i
+  uint32_t voff[2 * T];  // this lane's byte offset for its DMA i
 };
 
 // Rows [row_lo, row_hi) of the layout (a wgrad's summed rows), the tile's
@@ -90,10 +91,10 @@ __device__ __forceinline__ i32x4 bg_rsrc(const void* p, int64_t bytes) {
 
 // Fragment of 32 rows or columns (slab `sl` of the operand) for summed
 // elements [16 t + 8 h, +8) of the stage at `st`.
-template <int T>
+template <int BK>
 __device__ __forceinline__ bf16x8 bg_frag_rows(const uint8_t* st, int sl, int t, int li, int h) {
-  const int chunk = (2 * t + h) ^ bg_row_swz(li & 15);
-  return *reinterpret_cast<const bf16x8*>(st + sl * 2048 + li * 64 + chunk * 16);
+  const int chunk = (2 * t + h) ^ bg_row_swz<BK>(li);
+  return *reinterpret_cast<const bf16x8*>(st + sl * (64 * BK) + li * (2 * BK) + chunk * 16);
 }
 template <int T>
 __device__ __forceinline__ bf16x8 bg_frag_cols(uint8_t* st, int sl, int t, int lane) {
@@ -107,62 +108,76 @@ __device__ __forceinline__ bf16x8 bg_frag_cols(uint8_t* st, int sl, int t, int l
   return __builtin_bit_cast(bf16x8, v);
 }
 
+// Blocks of a tile shape that share a CU's 160 KiB, and the LDS each gets:
+// the stage ring, and for a gathered wgrad each wave's ring of row indices.
+template <int TM, int TN>
+constexpr int bg_blocks() { return TM + TN > 6 ? 1 : (TM + TN > 2 ? 2 : 3); }
+template <int MODE>
+constexpr int bg_index_ring() { return MODE == BG_WGRAD ? 4 * 8 * 256 : 0; }
+template <int TM, int TN>
+constexpr int bg_lds() { return 160 * 1024 / bg_blocks<TM, TN>() / 1024 * 1024; }
+// Stages of `bytes` the ring holds: a tile with few rows keeps more of them
+// in flight.
 template <int MODE, int TM, int TN>
-constexpr int bg_stage() { return (TM + TN) * 4096; }
-// LDS of a block: the stage ring, and for a gathered wgrad each wave's ring
-// of the row indices of 8 stages
-template <int MODE, int TM, int TN>
-constexpr int bg_lds() { return BG_BUFS * bg_stage<MODE, TM, TN>() + (MODE == BG_WGRAD ? 4 * 8 * 256 : 0); }
+constexpr int bg_bufs(int bytes) {
+  const int n = (bg_lds<TM, TN>() - bg_index_ring<MODE>()) / bytes;
+  const int most = MODE == BG_WGRAD ? 4 : 6;
+  return n < most ? n : most;
+}
 
-template <int MODE, int TM, int TN, int VS>
+template <int MODE, int TM, int TN, int BK, int VS>
 __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgOperand<TM>& oa, BgOperand<TN>& ob,
                                         uint8_t* lds, int w, int lane) {
   typedef BgMode<MODE> M;
-  constexpr int STAGE = bg_stage<MODE, TM, TN>();
-  constexpr int AT = TM * 4096;  // the stage's B follows its A
-  constexpr int NA = M::a_cols ? TM : VS;
+  constexpr int TA = M::a_cols ? TM : VS;  // A slabs of a stage
+  constexpr int NA = TA * BK / 32, NC = NA + TN * BK / 32;  // DMA instructions of this wave per stage
+  constexpr int STAGE = NC * 4096;
+  constexpr int NB = bg_bufs<MODE, TM, TN>(STAGE);
+  static_assert(NB >= 2, "a stage in use and one in flight");
+  constexpr int AT = NA * 4096;  // the stage's B follows its A
+  constexpr int NT = BK / 16;    // MFMA steps of a stage
   const int li = lane & 31, h = lane >> 5, wr = w >> 1, wc = w & 1;
   const uint32_t lbase = (uint32_t)(uintptr_t)lds;
   const bool gather = MODE == BG_WGRAD && p.row_index != nullptr;
-  const int nst = (int)((tl.K + BG_BK - 1) / BG_BK);
+  const int nst = (int)((tl.K + BK - 1) / BK);
   // gathered wgrad: DMA of the row indices of stage s into this wave's ring
-  const uint32_t ring = BG_BUFS * STAGE + (uint32_t)w * 8 * 256;
+  const uint32_t ring = NB * STAGE + (uint32_t)w * 8 * 256;
   auto issue_index = [&](int s) {
-    const int64_t left = min((int64_t)BG_BK, max((int64_t)0, tl.K - (int64_t)s * BG_BK));
-    const i32x4 ri = bg_rsrc(p.row_index + tl.row_lo + (int64_t)s * BG_BK, left * 4);
+    const int64_t left = min((int64_t)BK, max((int64_t)0, tl.K - (int64_t)s * BK));
+    const i32x4 ri = bg_rsrc(p.row_index + tl.row_lo + (int64_t)s * BK, left * 4);
     dma4(ri, (uint32_t)lane * 4, 0, lbase + ring + (uint32_t)(s & 7) * 256);
   };
   // this lane's rows of its DMAs of B in a stage, from the ring
   constexpr int RPI = 8 / TN;  // summed rows an instruction covers
-  auto gather_rows = [&](int s, int32_t (&idx)[TN]) {
+  auto gather_rows = [&](int s, int32_t (&idx)[NC - NA]) {
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
+    for (int i = 0; i < NC - NA; ++i) {
       const int r = (4 * i + w) * RPI + lane / (8 * TN);
       idx[i] = *reinterpret_cast<const int32_t*>(lds + ring + (s & 7) * 256 + r * 4);
     }
   };
   // What the DMAs of stage s share (a stage past the last has no summed
   // elements, so its DMAs write zeros), and DMA k of the stage.
-  constexpr int NC = NA + TN;  // DMA instructions of this wave per stage
   struct Issue {
     i32x4 ra, rb;
     uint32_t at, soff;
     bool in;  // row operands: this lane's chunk exists
     int s;
   };
-  const int chunk8 = 8 * ((lane & 3) ^ bg_row_swz(lane >> 2));
-  auto issue_at = [&](int s) {
+  constexpr int CPR = BK / 8;  // chunks of a row operand's LDS row
+  const int chunk8 = 8 * ((lane % CPR) ^ bg_row_swz<BK>(64 / CPR * w + lane / CPR));
+  auto issue_at = [&](int s, int buf) {
     Issue q;
     q.s = s;
-    q.at = lbase + (uint32_t)(s & (BG_BUFS - 1)) * STAGE + (uint32_t)w * 1024;
-    q.soff = (uint32_t)s * (BG_BK * 2);
-    q.in = (int64_t)s * BG_BK + chunk8 < tl.K;
-    const int64_t left = min((int64_t)BG_BK, max((int64_t)0, tl.K - (int64_t)s * BG_BK));
-    q.ra = M::a_cols ? bg_rsrc(oa.base + (int64_t)s * BG_BK * oa.stride, left * oa.stride) : oa.rsrc;
-    q.rb = M::b_cols && !gather ? bg_rsrc(ob.base + (int64_t)s * BG_BK * ob.stride, left * ob.stride) : ob.rsrc;
+    q.at = lbase + (uint32_t)buf * STAGE + (uint32_t)w * 1024;
+    q.soff = (uint32_t)s * (BK * 2);
+    q.in = (int64_t)s * BK + chunk8 < tl.K;
+    const int64_t left = min((int64_t)BK, max((int64_t)0, tl.K - (int64_t)s * BK));
+    q.ra = M::a_cols ? bg_rsrc(oa.base + (int64_t)s * BK * oa.stride, left * oa.stride) : oa.rsrc;
+    q.rb = M::b_cols && !gather ? bg_rsrc(ob.base + (int64_t)s * BK * ob.stride, left * ob.stride) : ob.rsrc;
     return q;
   };
-  auto issue_one = [&](const Issue& q, const int32_t (&idx)[TN], int k) {
+  auto issue_one = [&](const Issue& q, const int32_t (&idx)[NC - NA], int k) {
     if (k < NA) {
       if constexpr (M::a_cols) dma16(q.ra, oa.voff[k], 0, q.at + k * 4096);
       else dma16(q.ra, q.in ? oa.voff[k] : BG_OOB, q.soff, q.at + k * 4096);
@@ -175,19 +190,19 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
     } else if (!gather) {
       dma16(q.rb, ob.voff[i], 0, at);
     } else {
-      const int64_t r = (int64_t)q.s * BG_BK + (4 * i + w) * RPI + lane / (8 * TN);
+      const int64_t r = (int64_t)q.s * BK + (4 * i + w) * RPI + lane / (8 * TN);
       const bool in = r < tl.K && idx[i] >= 0 && idx[i] < p.a_rows && ob.voff[i] != BG_OOB;
       dma16(q.rb, in ? (uint32_t)idx[i] * (uint32_t)ob.stride + ob.voff[i] : BG_OOB, 0, at);
     }
   };
-  // fragment k (A slabs, then B slabs) of half t of stage s
-  auto read_one = [&](int s, int t, bf16x8 (&fa)[VS], bf16x8 (&fb)[TN], int k) {
-    uint8_t* st = lds + (s & (BG_BUFS - 1)) * STAGE;
+  // fragment k (A slabs, then B slabs) of MFMA step t of the stage in buffer buf
+  auto read_one = [&](int buf, int t, bf16x8 (&fa)[VS], bf16x8 (&fb)[TN], int k) {
+    uint8_t* st = lds + buf * STAGE;
     if (k < VS)
-      fa[k] = M::a_cols ? bg_frag_cols<TM>(st, 2 * k + wr, t, lane) : bg_frag_rows<TM>(st, 2 * k + wr, t, li, h);
+      fa[k] = M::a_cols ? bg_frag_cols<TM>(st, 2 * k + wr, t, lane) : bg_frag_rows<BK>(st, 2 * k + wr, t, li, h);
     else
       fb[k - VS] = M::b_cols ? bg_frag_cols<TN>(st + AT, TN * wc + k - VS, t, lane)
-                             : bg_frag_rows<TN>(st + AT, TN * wc + k - VS, t, li, h);
+                             : bg_frag_rows<BK>(st + AT, TN * wc + k - VS, t, li, h);
   };
   f32x16 acc[VS][TN];
 #pragma unroll
@@ -209,39 +224,44 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
     }
   };
 
-  int32_t idx[TN] = {};
+  int32_t idx[NC - NA] = {};
   if (gather) {
-    for (int s = 0; s < 4; ++s) issue_index(s);
+    for (int s = 0; s < NB; ++s) issue_index(s);
     wait_vmcnt<0>();
   }
-  for (int s = 0; s < BG_BUFS; ++s) {
+  for (int s = 0; s < NB; ++s) {
     if (gather) gather_rows(s, idx);
-    const Issue q = issue_at(s);
+    const Issue q = issue_at(s, s);
 #pragma unroll
     for (int k = 0; k < NC; ++k) issue_one(q, idx, k);
-    if (gather) issue_index(s + 4);
+    if (gather) issue_index(s + NB);
   }
   bf16x8 fa[2][VS], fb[2][TN];
-  if (gather) wait_vmcnt<3 * (NC + 1)>();
-  else wait_vmcnt<3 * NC>();
+  if (gather) wait_vmcnt<(NB - 1) * (NC + 1)>();
+  else wait_vmcnt<(NB - 1) * NC>();
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
   for (int k = 0; k < VS + TN; ++k) read_one(0, 0, fa[0], fb[0], k);
+  int cur = 0;
   for (int s = 0; s < nst; ++s) {
-    if (gather) gather_rows(s + 4, idx);
-    mma(fa[0], fb[0], VS + TN, [&](int k) { read_one(s, 1, fa[1], fb[1], k); });
+    const int nxt = cur + 1 == NB ? 0 : cur + 1;
+    if (gather) gather_rows(s + NB, idx);
+#pragma unroll
+    for (int t = 0; t + 1 < NT; ++t)
+      mma(fa[t & 1], fb[t & 1], VS + TN, [&](int k) { read_one(cur, t + 1, fa[(t + 1) & 1], fb[(t + 1) & 1], k); });
     // every read of stage s has landed and stage s + 1 is there: after the
     // barrier, for all four waves
     wait_lgkmcnt0();
-    if (gather) wait_vmcnt<2 * (NC + 1)>();
-    else wait_vmcnt<2 * NC>();
+    if (gather) wait_vmcnt<(NB - 2) * (NC + 1)>();
+    else wait_vmcnt<(NB - 2) * NC>();
     asm volatile("s_barrier" ::: "memory");
-    const Issue q = issue_at(s + 4);
+    const Issue q = issue_at(s + NB, cur);
     mma(fa[1], fb[1], VS + TN + NC, [&](int k) {
-      if (k < VS + TN) read_one(s + 1, 0, fa[0], fb[0], k);
+      if (k < VS + TN) read_one(nxt, 0, fa[0], fb[0], k);
       else issue_one(q, idx, k - VS - TN);
     });
-    if (gather) issue_index(s + 8);
+    if (gather) issue_index(s + 2 * NB);
+    cur = nxt;
   }
   wait_lgkmcnt0();
   wait_vmcnt<0>();
@@ -250,7 +270,7 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
   // Epilogue through LDS, slab by slab, in a region of this wave's own: 16
   // bytes a lane and whole row segments per store instruction.
   constexpr int RS = 128 * TN + 32;  // bytes of an LDS row (the pad parts the lane halves' banks)
-  static_assert(4 * 32 * RS <= bg_lds<MODE, TM, TN>(), "epilogue fits the ring");
+  static_assert(4 * 32 * RS <= bg_lds<TM, TN>(), "epilogue fits the ring");
   float* t = reinterpret_cast<float*>(lds + w * 32 * RS);
   const int64_t N = MODE == BG_FORWARD ? p.n : p.k;
   const int es = p.y_bf ? 2 : 4;
@@ -310,11 +330,95 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
   }
 }
 
-template <int MODE, int TM, int TN>
-__global__ __launch_bounds__(256) void bf16_tile_kernel(Bf16Args p) {
+// The block's tile.  Block b runs on XCD b % 8 (blocks are dealt round robin);
+// an XCD takes an eighth of the heavy tiles (more than half of their 64-row
+// slabs hold rows) and an eighth of the light ones, each in expert order,
+// so that neighbours share operand panels in its L2 and the eighths cost
+// alike.  Light tiles stream weights and heavy ones keep the MFMAs busy: the
+// light ones are mixed evenly among the heavy ones, but for an eighth of all
+// tiles kept for the end, where short tiles level the finish.  An expert's
+// heavy tiles go in bands of 4 m-tiles.  Every wave derives this from the
+// device offsets by wave scans in registers (G experts in NSEG segments of
+// 64 lanes).  False: no tile (block-uniform).
+template <int NSEG, int TM, int TN>
+__device__ __forceinline__ bool bg_schedule(const int32_t* offsets, int G, int64_t m_total, int tn, int lane, TileRange& out) {
+  constexpr int BM = 64 * TM;
+  const int32_t mt = (int32_t)m_total;
+  int32_t lo[NSEG], hi[NSEG], eh[NSEG], el[NSEG];
+#pragma unroll
+  for (int i = 0; i < NSEG; ++i)
+    if (64 * i < G) {
+      lo[i] = offsets[min(64 * i + lane, G)];
+      hi[i] = offsets[min(64 * i + lane + 1, G)];
+    }
+  int32_t nh = 0, nl = 0;
+#pragma unroll
+  for (int i = 0; i < NSEG; ++i) {
+    eh[i] = el[i] = 0x7FFFFFFF;
+    if (64 * i >= G) continue;
+    const int32_t a = min(max(lo[i], 0), mt), rows = min(max(hi[i], a), mt) - a;
+    lo[i] = a;
+    hi[i] = a + rows;
+    const int32_t slabs = rows / 64 + (rows % 64 != 0), rem = slabs % TM;
+    const bool in = 64 * i + lane < G;
+    const int32_t ch = in ? slabs / TM + (2 * rem > TM) : 0, cl = in && rem > 0 && 2 * rem <= TM;
+    const int32_t ih = wave_incl_scan(ch), il = wave_incl_scan(cl);
+    if (in) {
+      eh[i] = nh + ih - ch;
+      el[i] = nl + il - cl;
+    }
+    nh += __builtin_amdgcn_readlane(ih, 63);
+    nl += __builtin_amdgcn_readlane(il, 63);
+  }
+  const int x = (int)(blockIdx.x % 8), j = (int)(blockIdx.x / 8);
+  const int64_t th = (int64_t)nh * tn, tl = (int64_t)nl * tn;
+  const int h0 = (int)(th * x / 8), H = (int)(th * (x + 1) / 8) - h0;
+  const int l0 = (int)(tl * x / 8), L = (int)(tl * (x + 1) / 8) - l0;
+  if (j >= H + L) return false;
+  const int mixed = H + L - min(L, (H + L) / 8);  // H <= mixed
+  // heavy tiles among the first j: ceil(j H / mixed)
+  auto before = [&](int q) { return q >= mixed ? H : (int)(((int64_t)q * H + mixed - 1) / mixed); };
+  const int hb = before(j);
+  const bool heavy = before(j + 1) > hb;
+  const int idx = heavy ? h0 + hb : l0 + j - hb;
+  int m = idx / tn, n = idx % tn;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < NSEG; ++i)
+    if (64 * i < G) count += __popcll(__ballot((heavy ? eh[i] : el[i]) <= m));
+  const int g = count - 1, ln = g & 63;
+  int32_t lo_s = lo[0], hi_s = hi[0], eh_s = eh[0];
+#pragma unroll
+  for (int i = 1; i < NSEG; ++i)
+    if ((g >> 6) == i) { lo_s = lo[i]; hi_s = hi[i]; eh_s = eh[i]; }
+  const int32_t rlo = __builtin_amdgcn_readlane(lo_s, ln), rhi = __builtin_amdgcn_readlane(hi_s, ln);
+  int64_t first;
+  if (heavy) {
+    const int32_t e0 = __builtin_amdgcn_readlane(eh_s, ln);
+    const int32_t slabs = (rhi - rlo) / 64 + ((rhi - rlo) % 64 != 0);
+    const int mts = slabs / TM + (2 * (slabs % TM) > TM);
+    const int q = idx - e0 * tn;  // within the expert's mts x tn heavy tiles
+    const int band = q / (4 * tn), within = q % (4 * tn), bh = min(4, mts - 4 * band);
+    m = 4 * band + within % bh;
+    n = within / bh;
+    first = (int64_t)rlo + (int64_t)m * BM;
+  } else {
+    const int32_t slabs = (rhi - rlo) / 64 + ((rhi - rlo) % 64 != 0);
+    first = (int64_t)rlo + (int64_t)(slabs / TM) * BM;
+  }
+  out.g = g;
+  out.row_lo = first;
+  out.row_hi = min((int64_t)rhi, first + BM);
+  out.n0 = (int64_t)n * 64 * TN;
+  return out.row_lo < out.row_hi;
+}
+
+template <int MODE, int TM, int TN, int BK>
+__global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void bf16_tile_kernel(Bf16Args p) {
   typedef BgMode<MODE> M;
   constexpr int BM = 64 * TM, BN = 64 * TN;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds<MODE, TM, TN>()];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds<TM, TN>()];
+  constexpr int D = BK / 32, CPR = BK / 8;  // DMAs per slab and wave; chunks of a row operand's LDS row
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   BgTile tl;
   BgOperand<TM> oa;
@@ -337,7 +441,7 @@ __global__ __launch_bounds__(256) void bf16_tile_kernel(Bf16Args p) {
     oa.stride = p.n * 2;
     oa.base = reinterpret_cast<const uint8_t*>(p.a + lo * p.n + tl.m0);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+    for (int i = 0; i < TM * D; ++i) {
       const int row = (4 * i + w) * (8 / TM) + lane / (8 * TM);
       const int c = 8 * ((lane % (8 * TM)) ^ bg_col_swz<TM>(row));
       oa.voff[i] = tl.m0 + c < p.n ? (uint32_t)(row * oa.stride) + 2 * c : BG_OOB;
@@ -346,7 +450,7 @@ __global__ __launch_bounds__(256) void bf16_tile_kernel(Bf16Args p) {
     ob.base = reinterpret_cast<const uint8_t*>(p.b + (p.row_index ? 0 : lo * p.k) + tl.n0);
     if (p.row_index) ob.rsrc = bg_rsrc(p.b, p.a_rows * p.k * 2);
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
+    for (int i = 0; i < TN * D; ++i) {
       const int row = (4 * i + w) * (8 / TN) + lane / (8 * TN);
       const int c = 8 * ((lane % (8 * TN)) ^ bg_col_swz<TN>(row));
       const uint32_t at = p.row_index ? (uint32_t)(tl.n0 * 2) : (uint32_t)(row * ob.stride);
@@ -354,23 +458,24 @@ __global__ __launch_bounds__(256) void bf16_tile_kernel(Bf16Args p) {
     }
   } else {
     TileRange tr;
-    static_assert(SCHED_LDS_WORDS * 4 <= bg_lds<MODE, TM, TN>(), "tile schedule fits");
-    if (!schedule_tile<BM, BN>(p.t, lane, reinterpret_cast<int32_t*>(lds), tr)) return;  // block-uniform
-    __syncthreads();  // the schedule's LDS words have been read
+    const int tn = (int)(((MODE == BG_FORWARD ? p.n : p.k) + BN - 1) / BN);
+    const bool some = p.groups <= 256 ? bg_schedule<4, TM, TN>(p.offsets, p.groups, p.m_total, tn, lane, tr)
+                                      : bg_schedule<16, TM, TN>(p.offsets, p.groups, p.m_total, tn, lane, tr);
+    if (!some) return;  // block-uniform
     tl.row_lo = tr.row_lo;
     tl.row_hi = tr.row_hi;
     tl.n0 = tr.n0;
     tl.g = tr.g;
     tl.K = MODE == BG_FORWARD ? p.k : p.n;
     vs = (int)((tl.row_hi - tl.row_lo + 63) / 64);
-    // A: row operand, DMA i covers the tile's rows 16 (4 i + w) ..
+    // A: row operand, DMA i covers the tile's rows 64 / CPR (4 i + w) ..
     const uint32_t rowb = (uint32_t)tl.K * 2;
-    const int swz = 16 * ((lane & 3) ^ bg_row_swz(lane >> 2));
+    const int swz = 16 * ((lane % CPR) ^ bg_row_swz<BK>(64 / CPR * w + lane / CPR));
     if (p.row_index) oa.rsrc = bg_rsrc(p.a, p.a_rows * (int64_t)rowb);
     else oa.rsrc = bg_rsrc(p.a + tl.row_lo * tl.K, (tl.row_hi - tl.row_lo) * (int64_t)rowb);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int64_t row = tl.row_lo + 16 * (4 * i + w) + (lane >> 2);
+    for (int i = 0; i < TM * D; ++i) {
+      const int64_t row = tl.row_lo + 64 / CPR * (4 * i + w) + lane / CPR;
       int64_t src = gathered_row(p.row_index, p.a_rows, row, tl.row_hi);
       if (!p.row_index && src >= 0) src -= tl.row_lo;
       oa.voff[i] = src >= 0 ? (uint32_t)src * rowb + swz : BG_OOB;
@@ -379,7 +484,7 @@ __global__ __launch_bounds__(256) void bf16_tile_kernel(Bf16Args p) {
       ob.stride = p.k * 2;
       ob.base = reinterpret_cast<const uint8_t*>(p.b + (int64_t)tl.g * p.n * p.k + tl.n0);
 #pragma unroll
-      for (int i = 0; i < TN; ++i) {
+      for (int i = 0; i < TN * D; ++i) {
         const int row = (4 * i + w) * (8 / TN) + lane / (8 * TN);
         const int c = 8 * ((lane % (8 * TN)) ^ bg_col_swz<TN>(row));
         ob.voff[i] = tl.n0 + c < p.k ? (uint32_t)(row * ob.stride) + 2 * c : BG_OOB;
@@ -388,45 +493,91 @@ __global__ __launch_bounds__(256) void bf16_tile_kernel(Bf16Args p) {
       const int64_t cols = min((int64_t)BN, p.n - tl.n0);
       ob.rsrc = bg_rsrc(p.b + ((int64_t)tl.g * p.n + tl.n0) * p.k, cols * p.k * 2);
 #pragma unroll
-      for (int i = 0; i < TN; ++i) {
-        const int c = 16 * (4 * i + w) + (lane >> 2);
+      for (int i = 0; i < TN * D; ++i) {
+        const int c = 64 / CPR * (4 * i + w) + lane / CPR;
         ob.voff[i] = c < cols ? (uint32_t)c * rowb + swz : BG_OOB;
       }
     }
   }
   if constexpr (TM == 4) {
     switch (vs) {
-      case 4: bg_body<MODE, TM, TN, 4>(p, tl, oa, ob, lds, w, lane); break;
-      case 3: bg_body<MODE, TM, TN, 3>(p, tl, oa, ob, lds, w, lane); break;
-      case 2: bg_body<MODE, TM, TN, 2>(p, tl, oa, ob, lds, w, lane); break;
-      default: bg_body<MODE, TM, TN, 1>(p, tl, oa, ob, lds, w, lane); break;
+      case 4: bg_body<MODE, TM, TN, BK, 4>(p, tl, oa, ob, lds, w, lane); break;
+      case 3: bg_body<MODE, TM, TN, BK, 3>(p, tl, oa, ob, lds, w, lane); break;
+      case 2: bg_body<MODE, TM, TN, BK, 2>(p, tl, oa, ob, lds, w, lane); break;
+      default: bg_body<MODE, TM, TN, BK, 1>(p, tl, oa, ob, lds, w, lane); break;
     }
+  } else if constexpr (TM == 3) {
+    if (vs == 3) bg_body<MODE, TM, TN, BK, 3>(p, tl, oa, ob, lds, w, lane);
+    else if (vs == 2) bg_body<MODE, TM, TN, BK, 2>(p, tl, oa, ob, lds, w, lane);
+    else bg_body<MODE, TM, TN, BK, 1>(p, tl, oa, ob, lds, w, lane);
   } else if constexpr (TM == 2) {
-    if (vs == 2) bg_body<MODE, TM, TN, 2>(p, tl, oa, ob, lds, w, lane);
-    else bg_body<MODE, TM, TN, 1>(p, tl, oa, ob, lds, w, lane);
+    if (vs == 2) bg_body<MODE, TM, TN, BK, 2>(p, tl, oa, ob, lds, w, lane);
+    else bg_body<MODE, TM, TN, BK, 1>(p, tl, oa, ob, lds, w, lane);
   } else {
-    bg_body<MODE, TM, TN, 1>(p, tl, oa, ob, lds, w, lane);
+    bg_body<MODE, TM, TN, BK, 1>(p, tl, oa, ob, lds, w, lane);
   }
 }
 
-template <int MODE, int TM, int TN>
+template <int MODE, int TM, int TN, int BK>
 static void launch_tiles(const Bf16Args& a, hipStream_t str) {
   Bf16Args p = a;
   int64_t blocks;
   if (MODE == BG_WGRAD) {
     blocks = (int64_t)p.groups * ((p.n + 64 * TM - 1) / (64 * TM)) * ((p.k + 64 * TN - 1) / (64 * TN));
   } else {
-    p.t.m_total = p.m_total;
-    p.t.offsets = p.offsets;
-    p.t.groups = p.groups;
-    blocks = plan_tiles<64 * TM, 64 * TN>(p.t, MODE == BG_FORWARD ? p.n : p.k, true, 1, p.row_index != nullptr);
+    // at most a partial m-tile per expert that has rows, and an XCD's two
+    // ranges each rounded up
+    const int64_t mts = (p.m_total + 64 * TM - 1) / (64 * TM) + (p.groups < p.m_total ? p.groups : p.m_total);
+    blocks = 8 * ((mts * (((MODE == BG_FORWARD ? p.n : p.k) + 64 * TN - 1) / (64 * TN)) + 7) / 8 + 2);
   }
-  hipLaunchKernelGGL((bf16_tile_kernel<MODE, TM, TN>), dim3((unsigned)blocks), dim3(256), 0, str, p);
+  hipLaunchKernelGGL((bf16_tile_kernel<MODE, TM, TN, BK>), dim3((unsigned)blocks), dim3(256), 0, str, p);
 }
 
+// Tiles of a call in units of the CUs (an upper estimate: every expert may add
+// a partial m-tile), and the choice of tile from it.  The largest tile that
+// still gives every CU work is the fastest: it reads each operand least and
+// keeps the MFMAs busiest (one expert of 8192 rows, n = k = 8192: 256 x 256
+// 840 us, 192 x 128 938, 128 x 128 983, 64 x 128 1223, 64 x 64 1567), but a
+// grid of few tiles is bound by one tile's chain of stages, which is shorter
+// for a small tile (32 rows over 8 experts, n = k = 2048: 256 x 256 22 us,
+// 64 x 64 14).
+//  - forward: two 192 x 128 tiles a CU level ragged experts and hide each
+//    other's epilogues where the grid has fewer than three 256 x 256 tiles
+//    a CU (4096 rows over 8 experts, n = k = 2048: 44 us against 54), and
+//    experts with few rows are streams of weights, for which more blocks a CU
+//    hide more latency (1024 rows over 32 experts: 64 x 128 32 us against 52).
+//  - dgrad: W is read in rows of the output's columns, 512 contiguous bytes
+//    for 256 columns; two 128 x 256 tiles a CU beat one 256 x 256 tile
+//    (32768 rows over 128 experts, n = 2048, k = 768: 165 us against 189).
+//  - wgrad: two 256 x 128 tiles a CU: one writes its dW while the other
+//    multiplies (32768 rows over 128 experts, n = 1536, k = 2048, bf16: 354 us
+//    against 432 for 256 x 256).
 template <int MODE>
 static int launch_bf16(const Bf16Args& p, hipStream_t str) {
-  launch_tiles<MODE, 4, 4>(p, str);
+  const int64_t cus = nvfp4host::num_cus();
+  const int64_t rows = p.m_total / p.groups;  // of an expert, on average
+  auto tiles = [&](int TM, int TN) -> int64_t {
+    if (MODE == BG_WGRAD) return p.groups * ((p.n + 64 * TM - 1) / (64 * TM)) * ((p.k + 64 * TN - 1) / (64 * TN));
+    const int64_t partial = (p.groups < p.m_total ? p.groups : p.m_total) - 1;
+    return ((p.m_total + 64 * TM - 1) / (64 * TM) + partial) *
+           (((MODE == BG_FORWARD ? p.n : p.k) + 64 * TN - 1) / (64 * TN));
+  };
+  if constexpr (MODE == BG_FORWARD) {
+    if (tiles(4, 4) >= 3 * cus && rows >= 24) launch_tiles<MODE, 4, 4, 64>(p, str);
+    else if (tiles(3, 2) >= cus && rows >= 128) launch_tiles<MODE, 3, 2, 64>(p, str);
+    else if (tiles(2, 2) >= 2 * cus) launch_tiles<MODE, 2, 2, 64>(p, str);
+    else if (2 * tiles(1, 2) >= cus && rows >= 24) launch_tiles<MODE, 1, 2, 64>(p, str);
+    else launch_tiles<MODE, 1, 1, 64>(p, str);
+  } else if constexpr (MODE == BG_DGRAD) {
+    if (tiles(2, 4) >= cus) launch_tiles<MODE, 2, 4, 32>(p, str);
+    else if (2 * tiles(1, 2) >= cus && rows >= 24) launch_tiles<MODE, 1, 2, 64>(p, str);
+    else launch_tiles<MODE, 1, 1, 64>(p, str);
+  } else {
+    if (tiles(4, 2) >= cus) launch_tiles<MODE, 4, 2, 32>(p, str);
+    else if (tiles(2, 2) >= cus) launch_tiles<MODE, 2, 2, 64>(p, str);
+    else if (2 * tiles(1, 2) >= cus) launch_tiles<MODE, 1, 2, 64>(p, str);
+    else launch_tiles<MODE, 1, 1, 64>(p, str);
+  }
   return nvfp4host::launch_status();
 }
 
