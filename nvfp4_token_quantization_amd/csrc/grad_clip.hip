@@ -20,7 +20,10 @@ namespace nvfp4 {
 
 constexpr int CLIP_LIST = 96;        // tensors in one launch's arguments
 constexpr int CLIP_CHUNK = 8192;     // elements a block takes at a time
-constexpr int CLIP_BLOCKS = 1024;    // partial sums of one launch
+// Blocks, and partial sums, of one launch: three a CU (755 MB of fp32 and bf16
+// gradients, 512, 768, 1024, 2048 blocks: 452, 410, 419, 450 us; 5.5 TB/s over
+// the three passes at 768, the norm alone 133 us, 5.7 TB/s).
+constexpr int CLIP_BLOCKS = 768;
 
 struct ClipList {
   const void* in[CLIP_LIST];
@@ -58,34 +61,52 @@ __device__ __forceinline__ void chunk_at(const ClipList& l, int chunk, int& t, i
   hi = min(l.count[t], lo + CLIP_CHUNK);
 }
 
+// Elements [lo, hi) of a tensor to `slot` 8 at a time where the memory is
+// 16-byte aligned, and to `one` singly otherwise and at a ragged end.
+template <class Slot, class One>
+__device__ __forceinline__ void walk_chunk(int64_t lo, int64_t hi, bool wide, Slot&& slot, One&& one) {
+  int64_t e = lo;
+  if (wide) {
+    if (hi - lo == CLIP_CHUNK) {
+#pragma unroll
+      for (int i = 0; i < CLIP_CHUNK / 2048; ++i) slot(lo + 8 * (i * 256 + (int)threadIdx.x));
+      return;
+    }
+    const int n = (int)((hi - lo) / 8);
+    for (int i = threadIdx.x; i < n; i += 256) slot(lo + 8 * i);
+    e = lo + 8 * n;
+  }
+  for (e += threadIdx.x; e < hi; e += 256) one(e);
+}
+
 __global__ __launch_bounds__(256) void clip_squares_kernel(ClipList l, double* partial) {
   __shared__ double s[4];
-  double acc = 0.0;
+  double acc[2] = {0.0, 0.0};
   for (int chunk = blockIdx.x; chunk < l.first[l.n]; chunk += gridDim.x) {
     int t;
     int64_t lo, hi;
     chunk_at(l, chunk, t, lo, hi);
     const bool bf = (l.bf16[t >> 5] >> (t & 31)) & 1u;
     const uint8_t* base = static_cast<const uint8_t*>(l.in[t]);
-    if (((uintptr_t)base & 15) == 0 && hi - lo == CLIP_CHUNK) {
-#pragma unroll 4
-      for (int i = 0; i < CLIP_CHUNK / 2048; ++i) {
-        float v[8];
-        load8<true>(base + lo * (bf ? 2 : 4), bf, CLIP_CHUNK, i, 256, threadIdx.x, v);
+    walk_chunk(lo, hi, ((uintptr_t)base & 15) == 0,
+               [&](int64_t e) {
+                 float v[8];
+                 load8<true>(base + e * (bf ? 2 : 4), bf, 8, 0, 256, 0, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc = __builtin_fma((double)v[e], (double)v[e], acc);
-      }
-    } else {
-      for (int64_t e = lo + threadIdx.x; e < hi; e += 256) {
-        const double v = bf ? bf16_to_f32(reinterpret_cast<const uint16_t*>(base)[e]) : reinterpret_cast<const float*>(base)[e];
-        acc = __builtin_fma(v, v, acc);
-      }
-    }
+                 for (int i = 0; i < 8; ++i) acc[i & 1] = __builtin_fma((double)v[i], (double)v[i], acc[i & 1]);
+               },
+               [&](int64_t e) {
+                 const double v = bf ? bf16_to_f32(reinterpret_cast<const uint16_t*>(base)[e])
+                                     : reinterpret_cast<const float*>(base)[e];
+                 acc[0] = __builtin_fma(v, v, acc[0]);
+               });
   }
-  acc = block_sum_f64(acc, s);
-  if (threadIdx.x == 0) partial[blockIdx.x] = acc;
+  const double sum = block_sum_f64(acc[0] + acc[1], s);
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
+// Walks the chunks last to first: what the first pass read last is what the
+// memory-side cache still holds.
 __global__ __launch_bounds__(256) void clip_scale_kernel(ClipList l, const double* partial, int partials,
                                                          float max_norm, float* norm_out) {
   __shared__ double s[4];
@@ -95,15 +116,16 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(ClipList l, const doubl
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out) *norm_out = (float)norm;
   const double f = (double)max_norm / (norm + 1e-6);
   const float c = (float)(f > 1.0 ? 1.0 : f);  // a NaN norm gives a NaN factor
-  for (int chunk = blockIdx.x; chunk < l.first[l.n]; chunk += gridDim.x) {
+  for (int chunk = l.first[l.n] - 1 - (int)blockIdx.x; chunk >= 0; chunk -= gridDim.x) {
     int t;
     int64_t lo, hi;
     chunk_at(l, chunk, t, lo, hi);
     const bool bf = (l.bf16[t >> 5] >> (t & 31)) & 1u;
     const uint8_t* in = static_cast<const uint8_t*>(l.in[t]);
     uint8_t* out = static_cast<uint8_t*>(l.out[t]);
-    if ((((uintptr_t)in | (uintptr_t)out) & 15) == 0 && hi - lo == CLIP_CHUNK) {
-#pragma unroll 4
+    const bool wide = (((uintptr_t)in | (uintptr_t)out) & 15) == 0;
+    if (wide && hi - lo == CLIP_CHUNK) {
+#pragma unroll
       for (int i = 0; i < CLIP_CHUNK / 2048; ++i) {
         float v[8];
         load8<true>(in + lo * (bf ? 2 : 4), bf, CLIP_CHUNK, i, 256, threadIdx.x, v);
@@ -111,12 +133,20 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(ClipList l, const doubl
         for (int e = 0; e < 8; ++e) v[e] *= c;
         store8<true>(out + lo * (bf ? 2 : 4), bf, CLIP_CHUNK, i, 256, threadIdx.x, v);
       }
-    } else {
-      for (int64_t e = lo + threadIdx.x; e < hi; e += 256) {
-        if (bf) reinterpret_cast<uint16_t*>(out)[e] = to_bf16(bf16_to_f32(reinterpret_cast<const uint16_t*>(in)[e]) * c);
-        else reinterpret_cast<float*>(out)[e] = reinterpret_cast<const float*>(in)[e] * c;
-      }
+      continue;
     }
+    walk_chunk(lo, hi, wide,
+               [&](int64_t e) {
+                 float v[8];
+                 load8<true>(in + e * (bf ? 2 : 4), bf, 8, 0, 256, 0, v);
+#pragma unroll
+                 for (int i = 0; i < 8; ++i) v[i] *= c;
+                 store8<true>(out + e * (bf ? 2 : 4), bf, 8, 0, 256, 0, v);
+               },
+               [&](int64_t e) {
+                 if (bf) reinterpret_cast<uint16_t*>(out)[e] = to_bf16(bf16_to_f32(reinterpret_cast<const uint16_t*>(in)[e]) * c);
+                 else reinterpret_cast<float*>(out)[e] = reinterpret_cast<const float*>(in)[e] * c;
+               });
   }
 }
 
@@ -151,37 +181,44 @@ extern "C" int nvfp4_clip_grad_norm(const void* const* grads, void* const* out, 
   if (st) return st;
   hipStream_t str = (hipStream_t)stream;
   double* partial = static_cast<double*>(workspace);
-  int partials = 0;
   ClipList l;
-  // pass 0 sums squares, pass 1 scales (with nothing to scale: the norm only)
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t i = 0;
+  // the next list of up to CLIP_LIST tensors from i in direction `step`
+  auto next_list = [&](int64_t& i, int step) -> int64_t {
+    l.n = 0;
+    l.first[0] = 0;
+    for (uint32_t& b : l.bf16) b = 0u;
+    int64_t chunks = 0;  // at most 96 x 2^23
+    int64_t at[CLIP_LIST];
+    for (; i >= 0 && i < tensors && l.n < CLIP_LIST; i += step)
+      if (counts[i] > 0) at[l.n++] = i;
+    for (int j = 0; j < l.n; ++j) {
+      const int64_t k = at[step > 0 ? j : l.n - 1 - j];  // ascending either way
+      l.in[j] = grads[k];
+      l.out[j] = out ? out[k] : nullptr;
+      l.count[j] = counts[k];
+      if (types[k] == NVFP4_TYPE_BF16) l.bf16[j >> 5] |= 1u << (j & 31);
+      chunks += (counts[k] + CLIP_CHUNK - 1) / CLIP_CHUNK;
+      l.first[j + 1] = (int32_t)chunks;
+    }
+    return chunks < 1 ? 1 : (chunks < CLIP_BLOCKS ? chunks : CLIP_BLOCKS);
+  };
+  int partials = 0;
+  int64_t i = 0;
+  do {
+    const int64_t blocks = next_list(i, 1);
+    hipLaunchKernelGGL(clip_squares_kernel, dim3((unsigned)blocks), dim3(256), 0, str, l, partial + partials);
+    partials += (int)blocks;
+  } while (i < tensors);
+  if (out) {
+    i = tensors - 1;
     do {
-      l.n = 0;
-      l.first[0] = 0;
-      for (uint32_t& b : l.bf16) b = 0u;
-      int64_t chunks = 0;  // at most 96 x 2^23
-      for (; i < tensors && l.n < CLIP_LIST; ++i) {
-        if (counts[i] == 0) continue;
-        const int64_t c = (counts[i] + CLIP_CHUNK - 1) / CLIP_CHUNK;
-        l.in[l.n] = grads[i];
-        l.out[l.n] = out ? out[i] : nullptr;
-        l.count[l.n] = counts[i];
-        if (types[i] == NVFP4_TYPE_BF16) l.bf16[l.n >> 5] |= 1u << (l.n & 31);
-        chunks += c;
-        l.first[++l.n] = (int32_t)chunks;
-      }
-      const int64_t blocks = chunks < 1 ? 1 : (chunks < CLIP_BLOCKS ? chunks : CLIP_BLOCKS);
-      if (pass == 0) {
-        hipLaunchKernelGGL(clip_squares_kernel, dim3((unsigned)blocks), dim3(256), 0, str, l, partial + partials);
-        partials += (int)blocks;
-      } else {
-        if (!out) l.n = 0, l.first[0] = 0;
-        hipLaunchKernelGGL(clip_scale_kernel, dim3(out ? (unsigned)blocks : 1u), dim3(256), 0, str, l, partial, partials,
-                           max_norm, norm);
-        if (!out) break;
-      }
-    } while (i < tensors);
+      const int64_t blocks = next_list(i, -1);
+      hipLaunchKernelGGL(clip_scale_kernel, dim3((unsigned)blocks), dim3(256), 0, str, l, partial, partials, max_norm, norm);
+    } while (i >= 0);
+  } else {
+    l.n = 0;
+    l.first[0] = 0;
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(1), dim3(256), 0, str, l, partial, partials, max_norm, norm);
   }
   return nvfp4host::launch_status();
 }

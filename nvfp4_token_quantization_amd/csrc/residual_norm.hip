@@ -15,7 +15,9 @@
 // HBM-bound: every row is read once and stays in registers (W = ceil(d / 512)
 // waves hold 8 elements a thread, 16 past d = 8192).  The parameters are the
 // same for every row, so a block keeps them in registers and walks rows; the
-// next row's loads are issued before the current row's reductions.  The
+// next row's loads are issued before the current row's reductions.  A row's
+// bytes meet the copy rate of the card (16384 x 2560, fp32 block output, bf16
+// residual: forward 76 us, 5.5 TB/s; backward 118 us, 5.0 TB/s).  The
 // backward pass keeps its column sums in registers too, and writes one
 // partial row per block, which a second kernel adds in block order (no
 // atomics: the same bits on every call).
@@ -32,26 +34,48 @@ struct NormArgs {
   uint8_t *q, *sb;
   float* s;
   int64_t rows, d;
-  float scale, eps;
+  float scale, eps, inv_d;
   bool x_bf, r_bf, p_bf;
   bool gate_rows;  // gate [rows, d], else [d]
   // backward
   const void *dh, *dr;
   void *dx, *dr_out, *dgate;
   bool dx_bf;
-  float* part;  // [grid][3][d]: dw1, dw2, dg partial sums
+  float* part;  // [grid][2][d]: partial column sums
   float *dw1, *dw2, *dg;
 };
 
-__device__ __forceinline__ float rho_of(float sumsq, float d, float eps) { return 1.0f / __builtin_sqrtf(sumsq / d + eps); }
+// (mean + eps)^-1/2 within 2 ulp (the hardware's 1 ulp reciprocal root; below
+// the normal range the correctly rounded operations)
+__device__ __forceinline__ float rho_of(float sumsq, float inv_d, float eps) {
+  const float v = __builtin_fmaf(sumsq, inv_d, eps);
+  return v >= 0x1p-100f ? __builtin_amdgcn_rsqf(v) : 1.0f / __builtin_sqrtf(v);
+}
 
-template <int NV, bool VEC>
-__global__ __launch_bounds__(1024) void norm_forward_kernel(NormArgs p) {
+// How a kernel reads its rows: KIND 0 element by element with types known at
+// run time (any width and alignment), KIND 1 + x + 2 r in 16-byte pieces, x
+// and r telling whether x and the residual are bf16.
+template <int KIND>
+struct Rows {
+  static constexpr bool vec = KIND > 0;
+  static __device__ __forceinline__ bool x_bf(const NormArgs& p) { return KIND ? ((KIND - 1) & 1) != 0 : p.x_bf; }
+  static __device__ __forceinline__ bool r_bf(const NormArgs& p) { return KIND ? ((KIND - 1) & 2) != 0 : p.r_bf; }
+};
+
+// One slot of every row operand of a row: raw when it is fetched ahead.
+struct NormSlots {
+  RawSlot x, r, g, dh, dr;
+};
+
+template <int NV, int KIND, int MAXT>
+__global__ __launch_bounds__(MAXT) void norm_forward_kernel(NormArgs p) {
+  typedef Rows<KIND> R;
+  constexpr bool VEC = R::vec;
   __shared__ BlockSums<1> sums;
   __shared__ uint32_t smax[2][16];
   const int T = blockDim.x, tid = threadIdx.x, W = T >> 6;
   const int64_t d = p.d;
-  const float fd = (float)d;
+  const bool xb = R::x_bf(p), rb = R::r_bf(p);
   float w1[NV][8], w2[NV][8], gc[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -64,23 +88,38 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormArgs p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) gc[v][i] *= p.scale;
   }
+  NormSlots nx[NV];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      load_raw(row_at(p.x, xb, row, d), xb, d, v, T, tid, nx[v].x);
+      if (p.residual) load_raw(row_at(p.residual, rb, row, d), rb, d, v, T, tid, nx[v].r);
+      if (p.gate_rows) load_raw(row_at(p.gate, p.p_bf, row, d), p.p_bf, d, v, T, tid, nx[v].g);
+    }
+  };
+  if (VEC) fetch(blockIdx.x);
   int slot = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     float b[NV][8], r[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      load8<VEC>(row_at(p.x, p.x_bf, row, d), p.x_bf, d, v, T, tid, b[v]);
-      if (p.residual) load8<VEC>(row_at(p.residual, p.r_bf, row, d), p.r_bf, d, v, T, tid, r[v]);
-      else
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[v][i] = 0.0f;
+      for (int i = 0; i < 8; ++i) r[v][i] = 0.0f;
+      if (VEC) {
+        decode_raw(nx[v].x, xb, b[v]);
+        if (p.residual) decode_raw(nx[v].r, rb, r[v]);
+        if (p.gate_rows) decode_raw(nx[v].g, p.p_bf, gc[v]);
+      } else {
+        load8<false>(row_at(p.x, xb, row, d), xb, d, v, T, tid, b[v]);
+        if (p.residual) load8<false>(row_at(p.residual, rb, row, d), rb, d, v, T, tid, r[v]);
+        if (p.gate_rows) load8<false>(row_at(p.gate, p.p_bf, row, d), p.p_bf, d, v, T, tid, gc[v]);
+      }
       if (p.gate_rows) {
-        float g[8];
-        load8<VEC>(row_at(p.gate, p.p_bf, row, d), p.p_bf, d, v, T, tid, g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) gc[v][i] = g[i] * p.scale;
+        for (int i = 0; i < 8; ++i) gc[v][i] *= p.scale;
       }
     }
+    if (VEC && row + gridDim.x < p.rows) fetch(row + gridDim.x);
     if (p.post_w) {
       float ss[1] = {0.0f};
 #pragma unroll
@@ -89,7 +128,7 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormArgs p) {
         for (int i = 0; i < 8; ++i) ss[0] = __builtin_fmaf(b[v][i], b[v][i], ss[0]);
       block_sum<1>(ss, W, slot, sums);
       slot ^= 1;
-      const float rho = rho_of(ss[0], fd, p.eps);
+      const float rho = rho_of(ss[0], p.inv_d, p.eps);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -100,9 +139,9 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormArgs p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         r[v][i] = __builtin_fmaf(gc[v][i], b[v][i], r[v][i]);
-        if (p.r_bf) r[v][i] = bf16_to_f32(to_bf16(r[v][i]));
+        if (rb) r[v][i] = bf16_to_f32(to_bf16(r[v][i]));
       }
-      if (p.r_out) store8<VEC>(row_at(p.r_out, p.r_bf, row, d), p.r_bf, d, v, T, tid, r[v]);
+      if (p.r_out) store8<VEC>(row_at(p.r_out, rb, row, d), rb, d, v, T, tid, r[v]);
     }
     if (!p.norm_w) continue;
     float ss[1] = {0.0f};
@@ -111,7 +150,7 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormArgs p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss[0] = __builtin_fmaf(r[v][i], r[v][i], ss[0]);
     block_sum<1>(ss, W, slot, sums);
-    const float rho = rho_of(ss[0], fd, p.eps);
+    const float rho = rho_of(ss[0], p.inv_d, p.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
 #pragma unroll
@@ -157,119 +196,214 @@ __global__ __launch_bounds__(1024) void norm_forward_kernel(NormArgs p) {
   }
 }
 
-template <int NV, bool VEC>
-__global__ __launch_bounds__(1024) void norm_backward_kernel(NormArgs p) {
-  __shared__ BlockSums<3> sums3;
-  __shared__ BlockSums<1> sums1;
+// One pass, one reduction a row.  With q = a g w1 (a constant of a column) the
+// sum that db needs, sum(w1 dn b), splits into sums that need none of the
+// row's other results:
+//   sum(w1 dn b) = A + rho2 B - c2 C,   A = sum(q b dr'), B = sum(q b w2 dh),
+//   C = sum(q b r'),   c2 = rho2^3 / d sum(w2 dh r')
+// so all six sums of a row (with sum b^2, sum r'^2) meet in one exchange.
+// For a gate of the columns, dw1 and dg are both multiples of the column sums
+// of t b rho1: one running sum a column serves both.
+// A row's chain of dependent work, not its bytes, is what the waves of a CU
+// have to hide: with two exchanges, divisions and branches for every optional
+// part a row took about 3 us and 16384 x 2560 rows 250 us.  PLAIN: post and
+// next norm, both gradients, no gate by rows, known when compiled, and at
+// most 128 registers (four waves a SIMD).
+template <int NV, int KIND, int MAXT, bool PLAIN>
+__global__ __launch_bounds__(MAXT, PLAIN || MAXT > 512 ? 4 : 3) void norm_backward_kernel(NormArgs p) {
+  typedef Rows<KIND> R;
+  constexpr bool VEC = R::vec;
+  constexpr bool AHEAD = VEC && NV == 1;  // registers to fetch a row ahead
+  __shared__ BlockSums<6> sums;
   const int T = blockDim.x, tid = threadIdx.x, W = T >> 6;
   const int64_t d = p.d;
-  const float fd = (float)d;
-  float w1[NV][8], w2[NV][8], gc[NV][8], a1[NV][8], a2[NV][8], ag[NV][8];
+  const bool xb = R::x_bf(p), rb = R::r_bf(p);
+  const bool post = PLAIN || p.post_w, norm = PLAIN || p.norm_w, dr = PLAIN || p.dr, by_row = !PLAIN && p.gate_rows;
+  // w2 and q (by rows: a w1) of this thread's columns: in registers, or past
+  // d = 8192 in LDS, where each thread reads back what it wrote itself (with
+  // them in registers too, 2048 x 16384 spilled and took 220 us)
+  __shared__ f32x4 s_par[NV > 1 ? 4 * NV * MAXT : 1];
+  float w2r[8], qr[8], a1[NV][8], a2[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
+    float g[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      a1[v][i] = a2[v][i] = ag[v][i] = 0.0f;
-      w1[v][i] = w2[v][i] = gc[v][i] = 1.0f;
+      a1[v][i] = a2[v][i] = 0.0f;
+      w2r[i] = qr[i] = g[i] = 1.0f;
     }
-    if (p.post_w) load8<VEC>(p.post_w, p.p_bf, d, v, T, tid, w1[v]);
-    if (p.norm_w) load8<VEC>(p.norm_w, p.p_bf, d, v, T, tid, w2[v]);
-    if (p.gate && !p.gate_rows) load8<VEC>(p.gate, p.p_bf, d, v, T, tid, gc[v]);
+    if (norm) load8<VEC>(p.norm_w, p.p_bf, d, v, T, tid, w2r);
+    if (post) load8<VEC>(p.post_w, p.p_bf, d, v, T, tid, qr);
+    if (p.gate && !by_row) load8<VEC>(p.gate, p.p_bf, d, v, T, tid, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) qr[i] *= g[i] * p.scale;
+    if (NV > 1) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        s_par[(4 * v + k) * MAXT + tid] = (f32x4){w2r[4 * k], w2r[4 * k + 1], w2r[4 * k + 2], w2r[4 * k + 3]};
+        s_par[(4 * v + 2 + k) * MAXT + tid] = (f32x4){qr[4 * k], qr[4 * k + 1], qr[4 * k + 2], qr[4 * k + 3]};
+      }
+    }
   }
+  auto params = [&](int v, float (&w2)[8], float (&q)[8]) {
+    if (NV > 1) asm volatile("" ::: "memory");  // read here, not kept in registers over the rows
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w2[i] = NV > 1 ? s_par[(4 * v + i / 4) * MAXT + tid][i % 4] : w2r[i];
+      q[i] = NV > 1 ? s_par[(4 * v + 2 + i / 4) * MAXT + tid][i % 4] : qr[i];
+    }
+  };
+  NormSlots nx[NV];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      load_raw(row_at(p.x, xb, row, d), xb, d, v, T, tid, nx[v].x);
+      if (norm) {
+        load_raw(row_at(p.residual, rb, row, d), rb, d, v, T, tid, nx[v].r);
+        load_raw(row_at(p.dh, true, row, d), true, d, v, T, tid, nx[v].dh);
+      }
+      if (dr) load_raw(row_at(p.dr, rb, row, d), rb, d, v, T, tid, nx[v].dr);
+      if (by_row) load_raw(row_at(p.gate, p.p_bf, row, d), p.p_bf, d, v, T, tid, nx[v].g);
+    }
+  };
+  if (AHEAD) fetch(blockIdx.x);
   int slot = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, slot ^= 1) {
-    float b[NV][8], r[NV][8], dh[NV][8], t[NV][8];
+    float b[NV][8], r[NV][8], dh[NV][8], t[NV][8], g[NV][8];
+    if (VEC && !AHEAD) fetch(row);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      if (!norm) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[v][i] = r[v][i] = dh[v][i] = t[v][i] = 0.0f;
-      load8<VEC>(row_at(p.x, p.x_bf, row, d), p.x_bf, d, v, T, tid, b[v]);
-      if (p.norm_w) {
-        load8<VEC>(row_at(p.residual, p.r_bf, row, d), p.r_bf, d, v, T, tid, r[v]);
-        load8<VEC>(row_at(p.dh, true, row, d), true, d, v, T, tid, dh[v]);
+        for (int i = 0; i < 8; ++i) r[v][i] = dh[v][i] = 0.0f;
       }
-      if (p.dr) load8<VEC>(row_at(p.dr, p.r_bf, row, d), p.r_bf, d, v, T, tid, t[v]);
-      if (p.gate_rows) load8<VEC>(row_at(p.gate, p.p_bf, row, d), p.p_bf, d, v, T, tid, gc[v]);
-    }
-    float ss[3] = {0.0f, 0.0f, 0.0f};  // sum b^2, sum r'^2, sum w2 dh r'
+      if (!dr) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+        for (int i = 0; i < 8; ++i) t[v][i] = 0.0f;
+      }
+      if (VEC) {
+        decode_raw(nx[v].x, xb, b[v]);
+        if (norm) {
+          decode_raw(nx[v].r, rb, r[v]);
+          decode_raw(nx[v].dh, true, dh[v]);
+        }
+        if (dr) decode_raw(nx[v].dr, rb, t[v]);
+        if (by_row) decode_raw(nx[v].g, p.p_bf, g[v]);
+      } else {
+        load8<false>(row_at(p.x, xb, row, d), xb, d, v, T, tid, b[v]);
+        if (norm) {
+          load8<false>(row_at(p.residual, rb, row, d), rb, d, v, T, tid, r[v]);
+          load8<false>(row_at(p.dh, true, row, d), true, d, v, T, tid, dh[v]);
+        }
+        if (dr) load8<false>(row_at(p.dr, rb, row, d), rb, d, v, T, tid, t[v]);
+        if (by_row) load8<false>(row_at(p.gate, p.p_bf, row, d), p.p_bf, d, v, T, tid, g[v]);
+      }
+    }
+    if (AHEAD && row + gridDim.x < p.rows) fetch(row + gridDim.x);
+    float ss[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float w2[8], q[8];
+      params(v, w2, q);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        const float up = dh[v][i] * w2[i];
+        float qb = q[i] * b[v][i];
+        if (by_row) qb *= g[v][i];
         ss[0] = __builtin_fmaf(b[v][i], b[v][i], ss[0]);
         ss[1] = __builtin_fmaf(r[v][i], r[v][i], ss[1]);
-        ss[2] = __builtin_fmaf(dh[v][i] * w2[v][i], r[v][i], ss[2]);
+        ss[2] = __builtin_fmaf(up, r[v][i], ss[2]);
+        ss[3] = __builtin_fmaf(qb, t[v][i], ss[3]);
+        ss[4] = __builtin_fmaf(qb, up, ss[4]);
+        ss[5] = __builtin_fmaf(qb, r[v][i], ss[5]);
       }
-    block_sum<3>(ss, W, slot, sums3);
-    const float rho1 = p.post_w ? rho_of(ss[0], fd, p.eps) : 1.0f;
-    if (p.norm_w) {
-      const float rho2 = rho_of(ss[1], fd, p.eps);
-      const float c2 = rho2 * rho2 * (ss[2] / fd);
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          a2[v][i] = __builtin_fmaf(dh[v][i], r[v][i] * rho2, a2[v][i]);
-          t[v][i] = __builtin_fmaf(rho2, __builtin_fmaf(-r[v][i], c2, dh[v][i] * w2[v][i]), t[v][i]);
-        }
     }
-    float s1[1] = {0.0f};
+    block_sum<6>(ss, W, slot, sums);
+    const float rho1 = post ? rho_of(ss[0], p.inv_d, p.eps) : 1.0f;
+    const float rho2 = norm ? rho_of(ss[1], p.inv_d, p.eps) : 0.0f;
+    const float c2 = rho2 * rho2 * rho2 * (ss[2] * p.inv_d);
+    const float s1 = __builtin_fmaf(-c2, ss[5], __builtin_fmaf(rho2, ss[4], ss[3]));
+    const float c1 = post ? rho1 * rho1 * (s1 * p.inv_d) : 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      if (p.dr_out) store8<VEC>(row_at(p.dr_out, p.r_bf, row, d), p.r_bf, d, v, T, tid, t[v]);
-      float dgr[8];
+      float o[8], dg[8], w2[8], q[8];
+      params(v, w2, q);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float n0 = b[v][i] * rho1;                 // n without its weight
-        const float at = p.scale * t[v][i];
-        dgr[i] = at * (n0 * w1[v][i]);
-        ag[v][i] += dgr[i];
-        const float dn = at * gc[v][i];
-        a1[v][i] = __builtin_fmaf(dn, n0, a1[v][i]);
-        t[v][i] = dn * w1[v][i];
-        s1[0] = __builtin_fmaf(t[v][i], b[v][i], s1[0]);
+        if (norm) {
+          const float up = dh[v][i] * w2[i];
+          a2[v][i] = __builtin_fmaf(dh[v][i], r[v][i] * rho2, a2[v][i]);
+          t[v][i] = __builtin_fmaf(-r[v][i], c2, __builtin_fmaf(rho2, up, t[v][i]));
+        }
+        const float tn = t[v][i] * (b[v][i] * rho1);
+        float m = q[i] * t[v][i];
+        if (by_row) {
+          m *= g[v][i];
+          dg[i] = q[i] * tn;  // q is a w1 here
+          a1[v][i] = __builtin_fmaf(g[v][i], tn, a1[v][i]);
+        } else {
+          a1[v][i] += tn;
+        }
+        o[i] = rho1 * __builtin_fmaf(-b[v][i], c1, m);
       }
-      if (p.gate_rows && p.dgate) store8<VEC>(row_at(p.dgate, p.p_bf, row, d), p.p_bf, d, v, T, tid, dgr);
+      if (VEC) {
+        if (p.dr_out) store_raw(row_at(p.dr_out, rb, row, d), rb, d, v, T, tid, t[v]);
+        store_raw(row_at(p.dx, p.dx_bf, row, d), p.dx_bf, d, v, T, tid, o);
+        if (by_row && p.dgate) store_raw(row_at(p.dgate, p.p_bf, row, d), p.p_bf, d, v, T, tid, dg);
+      } else {
+        if (p.dr_out) store8<false>(row_at(p.dr_out, rb, row, d), rb, d, v, T, tid, t[v]);
+        store8<false>(row_at(p.dx, p.dx_bf, row, d), p.dx_bf, d, v, T, tid, o);
+        if (by_row && p.dgate) store8<false>(row_at(p.dgate, p.p_bf, row, d), p.p_bf, d, v, T, tid, dg);
+      }
     }
-    if (p.post_w) {
-      block_sum<1>(s1, W, slot, sums1);
-      const float c1 = rho1 * rho1 * (s1[0] / fd);
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[v][i] = rho1 * __builtin_fmaf(-b[v][i], c1, t[v][i]);
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) store8<VEC>(row_at(p.dx, p.dx_bf, row, d), p.dx_bf, d, v, T, tid, t[v]);
   }
-  float* part = p.part + (int64_t)blockIdx.x * 3 * d;
+  float* part = p.part + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    if (p.dw1) store8<VEC>(part, false, d, v, T, tid, a1[v]);
+    if (p.dw1 || p.dg) store8<VEC>(part, false, d, v, T, tid, a1[v]);
     if (p.dw2) store8<VEC>(part + d, false, d, v, T, tid, a2[v]);
-    if (p.dg) store8<VEC>(part + 2 * d, false, d, v, T, tid, ag[v]);
   }
 }
 
-// Column sums of the blocks' partial rows, in block order in fp32: 64 columns
-// a block, 16 row ranges of the partials added in order at the end.
+// Column sums of the blocks' partial rows in a fixed order: 64 columns a
+// block, 16 waves each over a sixteenth of the partial rows (8 loads in
+// flight), their sums added in order, and the columns' constants applied.
 __global__ __launch_bounds__(1024) void norm_columns_kernel(NormArgs p, int blocks) {
   __shared__ float red[16][64];
-  const int which = blockIdx.y;
-  float* out = which == 0 ? p.dw1 : (which == 1 ? p.dw2 : p.dg);
-  if (!out) return;
+  const int which = blockIdx.y;  // 0: sums of t b rho1, 1: of dh r' rho2
+  if (which == 0 ? !(p.dw1 || p.dg) : !p.dw2) return;
   const int lane = threadIdx.x & 63, part = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   const int per = (blocks + 15) / 16, b0 = part * per, b1 = min(blocks, b0 + per);
   float sum = 0.0f;
-  if (c < p.d)
-    for (int b = b0; b < b1; ++b) sum += p.part[((int64_t)b * 3 + which) * p.d + c];
+  if (c < p.d) {
+    const float* q = p.part + (int64_t)which * p.d + c;
+    const int64_t step = 2 * p.d;
+    int b = b0;
+    for (; b + 8 <= b1; b += 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = q[(b + i) * step];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i];
+    }
+    for (; b < b1; ++b) sum += q[b * step];
+  }
   red[part][lane] = sum;
   __syncthreads();
   if (part == 0 && c < p.d) {
     float t = 0.0f;
     for (int k = 0; k < 16; ++k) t += red[k][lane];
-    out[c] = t;
+    if (which == 1) {
+      p.dw2[c] = t;
+      return;
+    }
+    auto at = [&](const void* w) {
+      return p.p_bf ? bf16_to_f32(static_cast<const uint16_t*>(w)[c]) : static_cast<const float*>(w)[c];
+    };
+    const float st = p.scale * t;
+    if (p.dw1) p.dw1[c] = p.gate && !p.gate_rows ? at(p.gate) * st : st;
+    if (p.dg) p.dg[c] = p.post_w ? at(p.post_w) * st : st;
   }
 }
 
@@ -281,10 +415,35 @@ static int norm_waves(int64_t d) {
   return (int)((d + per - 1) / per);
 }
 
-// blocks of the backward pass (each walks rows and leaves one partial row)
+// Blocks of the backward pass: about ten waves a CU, since each block walks
+// rows and leaves one partial row (16384 x 2560, fp32 x, bf16 residual: 1, 2, 3
+// blocks a CU take 163, 118, 146 us, 4.97 TB/s at 2; 16384 x 1024: 106, 68, 58;
+// 16384 x 4096: 166, 172, 176).
 static int64_t norm_backward_blocks(int64_t rows, int64_t d) {
-  const int64_t cap = (int64_t)nvfp4host::num_cus() * (norm_waves(d) <= 8 ? 4 : 2);
+  const int64_t cap = (int64_t)nvfp4host::num_cus() * (norm_waves(d) <= 10 ? 10 / norm_waves(d) : 1);
   return rows < cap ? rows : cap;
+}
+
+template <int NV, int MAXT>
+static void launch_forward(const NormArgs& p, int kind, dim3 grid, dim3 block, hipStream_t s) {
+  switch (kind) {
+    case 0: hipLaunchKernelGGL((norm_forward_kernel<NV, 0, MAXT>), grid, block, 0, s, p); break;
+    case 1: hipLaunchKernelGGL((norm_forward_kernel<NV, 1, MAXT>), grid, block, 0, s, p); break;
+    case 2: hipLaunchKernelGGL((norm_forward_kernel<NV, 2, MAXT>), grid, block, 0, s, p); break;
+    case 3: hipLaunchKernelGGL((norm_forward_kernel<NV, 3, MAXT>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((norm_forward_kernel<NV, 4, MAXT>), grid, block, 0, s, p); break;
+  }
+}
+
+template <int NV, int MAXT, bool PLAIN>
+static void launch_backward(const NormArgs& p, int kind, dim3 grid, dim3 block, hipStream_t s) {
+  switch (kind) {
+    case 1: hipLaunchKernelGGL((norm_backward_kernel<NV, 1, MAXT, PLAIN>), grid, block, 0, s, p); break;
+    case 2: hipLaunchKernelGGL((norm_backward_kernel<NV, 2, MAXT, PLAIN>), grid, block, 0, s, p); break;
+    case 3: hipLaunchKernelGGL((norm_backward_kernel<NV, 3, MAXT, PLAIN>), grid, block, 0, s, p); break;
+    case 4: hipLaunchKernelGGL((norm_backward_kernel<NV, 4, MAXT, PLAIN>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((norm_backward_kernel<NV, 0, MAXT, false>), grid, block, 0, s, p); break;
+  }
 }
 
 static bool vec_rows(int64_t d, const void* const* ptrs, int n) {
@@ -340,26 +499,25 @@ extern "C" int nvfp4_residual_norm(const void* x, int x_type, const void* residu
   nvfp4::NormArgs p{};
   p.x = x; p.residual = residual; p.post_w = post_weight; p.gate = gate; p.norm_w = wants_h ? norm_weight : nullptr;
   p.r_out = residual_out; p.h = h; p.amax = amax; p.q = q; p.sb = sb; p.s = s;
-  p.rows = rows; p.d = d; p.scale = scale; p.eps = eps;
+  p.rows = rows; p.d = d; p.scale = scale; p.eps = eps; p.inv_d = 1.0f / (float)d;
   p.x_bf = x_type == NVFP4_TYPE_BF16; p.r_bf = residual_type == NVFP4_TYPE_BF16;
   p.p_bf = param_type == NVFP4_TYPE_BF16; p.gate_rows = gate && gate_rows;
   const int W = nvfp4::norm_waves(d);
-  const int64_t cap = (int64_t)nvfp4host::num_cus() * (32 / W > 16 ? 16 : (32 / W < 2 ? 2 : 32 / W));
+  // about 16 waves a CU (16384 x 2560, 2, 3, 4, 8 blocks a CU: 78, 76, 87, 86 us,
+  // 5.5 TB/s at 3; 32768 x 512, 2, 4, 8, 16: 59, 35, 27, 26)
+  const int64_t cap = (int64_t)nvfp4host::num_cus() * (16 / W);
   const dim3 grid((unsigned)(rows < cap ? rows : cap)), block(64 * W);
   hipStream_t str = (hipStream_t)stream;
-  if (d <= 8192) {
-    if (vec) hipLaunchKernelGGL((nvfp4::norm_forward_kernel<1, true>), grid, block, 0, str, p);
-    else hipLaunchKernelGGL((nvfp4::norm_forward_kernel<1, false>), grid, block, 0, str, p);
-  } else {
-    if (vec) hipLaunchKernelGGL((nvfp4::norm_forward_kernel<2, true>), grid, block, 0, str, p);
-    else hipLaunchKernelGGL((nvfp4::norm_forward_kernel<2, false>), grid, block, 0, str, p);
-  }
+  const int kind = vec ? 1 + (p.x_bf ? 1 : 0) + (p.r_bf ? 2 : 0) : 0;
+  if (W <= 8) nvfp4::launch_forward<1, 512>(p, kind, grid, block, str);
+  else if (d <= 8192) nvfp4::launch_forward<1, 1024>(p, kind, grid, block, str);
+  else nvfp4::launch_forward<2, 1024>(p, kind, grid, block, str);
   return nvfp4host::launch_status();
 }
 
 extern "C" int64_t nvfp4_residual_norm_backward_workspace(int64_t rows, int64_t d) {
   if (rows < 1 || d < 1 || d > nvfp4::NORM_MAX_D) return 0;
-  return nvfp4::norm_backward_blocks(rows, d) * 3 * d * (int64_t)sizeof(float);
+  return nvfp4::norm_backward_blocks(rows, d) * 2 * d * (int64_t)sizeof(float);
 }
 
 extern "C" int nvfp4_residual_norm_backward(const void* x, int x_type, const void* residual_out, int residual_type,
@@ -386,7 +544,7 @@ extern "C" int nvfp4_residual_norm_backward(const void* x, int x_type, const voi
     return NVFP4_ERROR_MISALIGNED;
   nvfp4::NormArgs p{};
   p.x = x; p.residual = residual_out; p.post_w = post_weight; p.gate = gate; p.norm_w = dh ? norm_weight : nullptr;
-  p.rows = rows; p.d = d; p.scale = scale; p.eps = eps;
+  p.rows = rows; p.d = d; p.scale = scale; p.eps = eps; p.inv_d = 1.0f / (float)d;
   p.x_bf = x_type == NVFP4_TYPE_BF16; p.r_bf = residual_type == NVFP4_TYPE_BF16;
   p.p_bf = param_type == NVFP4_TYPE_BF16; p.gate_rows = per_row_gate;
   p.dh = dh; p.dr = d_residual_out; p.dx = dx; p.dx_bf = dx_type == NVFP4_TYPE_BF16; p.dr_out = d_residual;
@@ -398,23 +556,25 @@ extern "C" int nvfp4_residual_norm_backward(const void* x, int x_type, const voi
   int st = nvfp4host::check_arch();
   if (st) return st;
   const int64_t blocks = rows > 0 ? nvfp4::norm_backward_blocks(rows, d) : 0;
-  if (columns && rows > 0 && (!workspace || workspace_bytes < blocks * 3 * d * (int64_t)sizeof(float)))
+  if (columns && rows > 0 && (!workspace || workspace_bytes < blocks * 2 * d * (int64_t)sizeof(float)))
     return NVFP4_ERROR_INVALID_VALUE;
   hipStream_t str = (hipStream_t)stream;
   if (rows > 0) {
     const void* ptrs[] = {x, residual_out, d_residual_out, d_residual, post_weight, gate, norm_weight, dh, dx, p.dgate};
     const bool vec = nvfp4::vec_rows(d, ptrs, 10);
-    const dim3 grid((unsigned)blocks), block(64 * nvfp4::norm_waves(d));
-    if (d <= 8192) {
-      if (vec) hipLaunchKernelGGL((nvfp4::norm_backward_kernel<1, true>), grid, block, 0, str, p);
-      else hipLaunchKernelGGL((nvfp4::norm_backward_kernel<1, false>), grid, block, 0, str, p);
-    } else {
-      if (vec) hipLaunchKernelGGL((nvfp4::norm_backward_kernel<2, true>), grid, block, 0, str, p);
-      else hipLaunchKernelGGL((nvfp4::norm_backward_kernel<2, false>), grid, block, 0, str, p);
-    }
+    const int W = nvfp4::norm_waves(d);
+    const dim3 grid((unsigned)blocks), block(64 * W);
+    const int kind = vec ? 1 + (p.x_bf ? 1 : 0) + (p.r_bf ? 2 : 0) : 0;
+    const bool plain = p.post_w && p.norm_w && p.dr && !p.gate_rows;
+    if (W <= 8 && plain) nvfp4::launch_backward<1, 512, true>(p, kind, grid, block, str);
+    else if (W <= 8) nvfp4::launch_backward<1, 512, false>(p, kind, grid, block, str);
+    else if (d <= 8192 && plain) nvfp4::launch_backward<1, 1024, true>(p, kind, grid, block, str);
+    else if (d <= 8192) nvfp4::launch_backward<1, 1024, false>(p, kind, grid, block, str);
+    else if (plain) nvfp4::launch_backward<2, 1024, true>(p, kind, grid, block, str);
+    else nvfp4::launch_backward<2, 1024, false>(p, kind, grid, block, str);
   }
   if (columns)
-    hipLaunchKernelGGL(nvfp4::norm_columns_kernel, dim3((unsigned)((d + 63) / 64), 3), dim3(1024), 0, str, p,
+    hipLaunchKernelGGL(nvfp4::norm_columns_kernel, dim3((unsigned)((d + 63) / 64), 2), dim3(1024), 0, str, p,
                        (int)blocks);
   return nvfp4host::launch_status();
 }

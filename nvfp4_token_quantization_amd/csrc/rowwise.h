@@ -68,6 +68,7 @@ __device__ __forceinline__ void load8(const void* row, bool is_bf16, int64_t d, 
 }
 
 // 8 fp32 values to slot v of the row at `row`, rounded once when it is bf16
+// (streaming stores)
 template <bool VEC>
 __device__ __forceinline__ void store8(void* row, bool is_bf16, int64_t d, int v, int T, int tid,
                                        const float (&o)[8]) {
@@ -76,11 +77,11 @@ __device__ __forceinline__ void store8(void* row, bool is_bf16, int64_t d, int v
     if (e >= d) return;
     if (is_bf16) {
       const u32x4 w = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])};
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(row) + e) = w;
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(row) + e));
     } else {
       f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(row) + e);
-      p[0] = (f32x4){o[0], o[1], o[2], o[3]};
-      p[1] = (f32x4){o[4], o[5], o[6], o[7]};
+      __builtin_nontemporal_store((f32x4){o[0], o[1], o[2], o[3]}, p);
+      __builtin_nontemporal_store((f32x4){o[4], o[5], o[6], o[7]}, p + 1);
     }
   } else {
 #pragma unroll
@@ -90,6 +91,46 @@ __device__ __forceinline__ void store8(void* row, bool is_bf16, int64_t d, int v
       if (is_bf16) static_cast<uint16_t*>(row)[e] = to_bf16(o[i]);
       else static_cast<float*>(row)[e] = o[i];
     }
+  }
+}
+
+// Slot v of a row that is read or written once (VEC), through a resource over
+// the row: slots past its end read as zeros and are not written, without a
+// branch.  Streaming accesses; the loads are raw, so that a caller issues them
+// a row ahead of their use and decodes them then.
+struct RawSlot {
+  u32x4 a, b;  // b: the second half of an fp32 slot
+};
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* row, bool is_bf16, int64_t d) {
+  return out_rsrc(reinterpret_cast<float*>(const_cast<void*>(row)), d * (is_bf16 ? 2 : 4));
+}
+__device__ __forceinline__ void load_raw(const void* row, bool is_bf16, int64_t d, int v, int T, int tid, RawSlot& o) {
+  const __amdgpu_buffer_rsrc_t r = row_rsrc(row, is_bf16, d);
+  const uint32_t at = (uint32_t)slot_elem<true>(v, 0, T, tid) * (is_bf16 ? 2 : 4);
+  o.a = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 2);
+  if (!is_bf16) o.b = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16, 0, 2);
+}
+__device__ __forceinline__ void decode_raw(const RawSlot& r, bool is_bf16, float (&o)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (is_bf16) {
+      o[2 * i] = __uint_as_float(r.a[i] << 16);
+      o[2 * i + 1] = __uint_as_float(r.a[i] & 0xFFFF0000u);
+    } else {
+      o[i] = __uint_as_float(r.a[i]);
+      o[4 + i] = __uint_as_float(r.b[i]);
+    }
+  }
+}
+__device__ __forceinline__ void store_raw(void* row, bool is_bf16, int64_t d, int v, int T, int tid, const float (&o)[8]) {
+  const __amdgpu_buffer_rsrc_t r = row_rsrc(row, is_bf16, d);
+  const uint32_t at = (uint32_t)slot_elem<true>(v, 0, T, tid) * (is_bf16 ? 2 : 4);
+  if (is_bf16) {
+    const u32x4 w = {pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])};
+    __builtin_amdgcn_raw_buffer_store_b128(w, r, at, 0, 2);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, (f32x4){o[0], o[1], o[2], o[3]}), r, at, 0, 2);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, (f32x4){o[4], o[5], o[6], o[7]}), r, at + 16, 0, 2);
   }
 }
 
