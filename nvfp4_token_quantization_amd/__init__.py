@@ -138,7 +138,13 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without building a Stream object (1.8 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev):
+    if _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(dev.index))
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
@@ -673,22 +679,22 @@ def nvfp4_bf16_grouped_wgrad(dy, x, offsets, row_index=None, add=None, out=None,
     return out
 
 
-def _norm_params(dev, rows, d, **params):
+def _norm_params(dev, rows, d, post_weight, gate, norm_weight):
     """Check the parameters of the residual norms (one dtype, [d]; the gate
     [d] or [rows, d]); returns (param dtype, gate is per row)."""
     dtype = None
-    for name, t in params.items():
+    for name, t in (("post_weight", post_weight), ("gate", gate), ("norm_weight", norm_weight)):
         if t is None:
             continue
         _dev(t, name, _FLOATS)
-        if tuple(t.shape) != (d,) and not (name == "gate" and tuple(t.shape) == (rows, d)):
+        if t.shape != (d,) and not (t is gate and t.shape == (rows, d)):
             raise ValueError("%s must have shape (%d,)%s (got %s)" % (
-                name, d, " or (%d, %d)" % (rows, d) if name == "gate" else "", tuple(t.shape)))
+                name, d, " or (%d, %d)" % (rows, d) if t is gate else "", tuple(t.shape)))
         if dtype is not None and t.dtype != dtype:
             raise TypeError("post_weight, gate and norm_weight must have one dtype (got %s and %s)" % (dtype, t.dtype))
         dtype = t.dtype
-        _same_device(dev, (name, t))
-    gate = params.get("gate")
+        if t.device != dev:
+            raise ValueError("%s must be on %s (got %s)" % (name, dev, t.device))
     return dtype or torch.float32, gate is not None and gate.dim() == 2
 
 
@@ -718,7 +724,7 @@ def nvfp4_residual_norm(x, residual=None, norm_weight=None, post_weight=None, ga
     _dev(x, "x", _FLOATS, 2)
     rows, d = x.shape
     dev = x.device
-    ptype, gate_rows = _norm_params(dev, rows, d, post_weight=post_weight, gate=gate, norm_weight=norm_weight)
+    ptype, gate_rows = _norm_params(dev, rows, d, post_weight, gate, norm_weight)
     if residual is not None:
         _like(residual, "residual", x, _FLOATS)
         if residual_dtype not in (None, residual.dtype):
@@ -775,7 +781,7 @@ def nvfp4_residual_norm_backward(x, residual, norm_weight=None, dh=None, d_resid
     _dev(x, "x", _FLOATS, 2)
     rows, d = x.shape
     dev = x.device
-    ptype, gate_rows = _norm_params(dev, rows, d, post_weight=post_weight, gate=gate, norm_weight=norm_weight)
+    ptype, gate_rows = _norm_params(dev, rows, d, post_weight, gate, norm_weight)
     _like(residual, "residual", x, _FLOATS)
     if dh is None and d_residual is None:
         raise ValueError("dh or d_residual must be given")
@@ -902,28 +908,37 @@ def nvfp4_clip_grad_norm(grads, max_norm, out=None, norm_only=False, workspace=N
     n = len(grads)
     if n == 0:
         raise ValueError("grads must hold at least one tensor")
-    dev = grads[0].device
+    dev = grads[0].device if isinstance(grads[0], torch.Tensor) else None
+    types, counts, ptrs = [], [], []
     for i, t in enumerate(grads):
-        _dev(t, "grads[%d]" % i, _FLOATS)
+        _dev(t, "a gradient", _FLOATS)
         if t.device != dev:
             raise ValueError("grads[%d] must be on %s (got %s)" % (i, dev, t.device))
+        types.append(_TYPES[t.dtype])
+        counts.append(t.numel())
+        ptrs.append(t.data_ptr())
+    outs = ptrs
     if norm_only:
         if out is not None:
             raise ValueError("norm_only takes no out")
-    elif out is None:
-        out = grads
-    else:
+        outs = None
+    elif out is not None:
         out = list(out)
         if len(out) != n:
             raise ValueError("out must have one tensor per gradient")
+        outs = []
         for i, (t, g) in enumerate(zip(out, grads)):
-            _out(t, "out[%d]" % i, tuple(g.shape), g.dtype, dev)
-    if out is not None:
-        _disjoint(grads, out)
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in grads])
-    outs = None if out is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in out])
-    counts = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
-    types = (ctypes.c_int32 * n)(*[_TYPES[t.dtype] for t in grads])
+            _dev(t, "an out tensor", (g.dtype,))
+            if t.shape != g.shape or t.device != dev:
+                raise ValueError("out[%d] must have shape %s on %s (got %s on %s)" % (i, tuple(g.shape), dev,
+                                                                                     tuple(t.shape), t.device))
+            outs.append(t.data_ptr())
+    if outs is not None:
+        _disjoint(ptrs, outs, [c * (2 if k else 4) for c, k in zip(counts, types)])
+        outs = (ctypes.c_void_p * n)(*outs)
+    ptrs = (ctypes.c_void_p * n)(*ptrs)
+    counts = (ctypes.c_int64 * n)(*counts)
+    types = (ctypes.c_int32 * n)(*types)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = torch.empty((lib().nvfp4_clip_grad_norm_workspace(n),), dtype=torch.uint8, device=dev)
@@ -937,19 +952,20 @@ def nvfp4_clip_grad_norm(grads, max_norm, out=None, norm_only=False, workspace=N
     return norm
 
 
-def _disjoint(grads, out):
+def _disjoint(grads, outs, sizes):
     """No output may share memory with another output or another gradient: it
-    would be read, or scaled twice, after it was written."""
-    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i)
-                   for i, t in enumerate(out) if t.numel())
-    for (_, end, _), (lo, _, i) in zip(spans, spans[1:]):
+    would be read, or scaled twice, after it was written.  grads and outs:
+    addresses, outs[i] of the same size in bytes as grads[i]."""
+    spans = sorted((p, p + size, i) for i, (p, size) in enumerate(zip(outs, sizes)) if size)
+    end = 0
+    for lo, hi, i in spans:
         if lo < end:
-            raise ValueError("out tensors must not overlap (tensor %d)" % i)
-    if out is grads:
+            raise ValueError("the tensors that are written must not overlap (tensor %d)" % i)
+        end = hi
+    if outs is grads:
         return
     starts = [s[0] for s in spans]
-    for i, g in enumerate(grads):
-        lo, hi = g.data_ptr(), g.data_ptr() + g.numel() * g.element_size()
-        k = bisect.bisect_left(starts, hi) - 1  # the last output that starts below the gradient's end
-        if g.numel() and k >= 0 and spans[k][1] > lo and (spans[k][0] != lo or spans[k][2] != i):
+    for i, (lo, size) in enumerate(zip(grads, sizes)):
+        k = bisect.bisect_left(starts, lo + size) - 1  # the last output that starts below the gradient's end
+        if size and k >= 0 and spans[k][1] > lo and (spans[k][0] != lo or spans[k][2] != i):
             raise ValueError("out must not overlap another gradient (tensor %d)" % i)

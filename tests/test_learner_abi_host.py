@@ -181,9 +181,9 @@ def test_binding_refuses_cpu_tensors_and_overlaps():
                 lambda: nv.nvfp4_moe_combine(x, i32), lambda: nv.nvfp4_clip_grad_norm([x], 1.0)):
         with pytest.raises(ValueError):
             bad()
-    t = torch.zeros(64)
-    nv._disjoint([t[:8], t[8:16]], [t[16:24], t[8:16]])
-    for grads, out in (([t[:8], t[4:12]], None), ([t[:8], t[:8]], None), ([t[:8], t[8:16]], [t[8:16], t[:8]]),
-                       ([t[:8], t[8:16]], [t[16:24], t[20:28]]), ([t[:8], t[8:16]], [t[4:12], t[32:40]])):
+    nv._disjoint([0, 32], [64, 32], [32, 32])
+    nv._disjoint([0, 16], [64, 64], [32, 0])
+    for grads, outs in (([0, 16], None), ([0, 0], None), ([0, 32], [32, 0]), ([0, 32], [64, 80]), ([0, 32], [16, 128]),
+                        ([0, 64], [64, 128])):
         with pytest.raises(ValueError):
-            nv._disjoint(grads, grads if out is None else out)
+            nv._disjoint(grads, grads if outs is None else outs, [32, 32])
