@@ -116,30 +116,32 @@ template <int MODE>
 constexpr int bg_index_ring() { return MODE == BG_WGRAD ? 4 * 8 * 256 : 0; }
 template <int TM, int TN>
 constexpr int bg_lds() { return 160 * 1024 / bg_blocks<TM, TN>() / 1024 * 1024; }
-// Stages of `bytes` the ring holds: a tile with few rows keeps more of them
-// in flight.
-template <int MODE, int TM, int TN>
+// Stages of `bytes` the ring of one of KG wave groups holds: a tile with few
+// rows keeps more of them in flight.
+template <int MODE, int TM, int TN, int KG>
 constexpr int bg_bufs(int bytes) {
-  const int n = (bg_lds<TM, TN>() - bg_index_ring<MODE>()) / bytes;
+  const int n = ((KG > 1 ? 160 * 1024 / KG : bg_lds<TM, TN>()) - bg_index_ring<MODE>()) / bytes;
   const int most = MODE == BG_WGRAD ? 4 : 6;
   return n < most ? n : most;
 }
 
-template <int MODE, int TM, int TN, int BK, int VS>
+// KG wave groups of four waves each sum their own range of `nst` stages, with a
+// ring of their own, and the first adds the others' tiles in order.
+template <int MODE, int TM, int TN, int BK, int KG, int VS>
 __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgOperand<TM>& oa, BgOperand<TN>& ob,
-                                        uint8_t* lds, int w, int lane) {
+                                        uint8_t* block_lds, int nst, int grp, int w, int lane) {
+  uint8_t* lds = block_lds + (KG > 1 ? grp * (160 * 1024 / KG) : 0);
   typedef BgMode<MODE> M;
   constexpr int TA = M::a_cols ? TM : VS;  // A slabs of a stage
   constexpr int NA = TA * BK / 32, NC = NA + TN * BK / 32;  // DMA instructions of this wave per stage
   constexpr int STAGE = NC * 4096;
-  constexpr int NB = bg_bufs<MODE, TM, TN>(STAGE);
+  constexpr int NB = bg_bufs<MODE, TM, TN, KG>(STAGE);
   static_assert(NB >= 2, "a stage in use and one in flight");
   constexpr int AT = NA * 4096;  // the stage's B follows its A
   constexpr int NT = BK / 16;    // MFMA steps of a stage
   const int li = lane & 31, h = lane >> 5, wr = w >> 1, wc = w & 1;
   const uint32_t lbase = (uint32_t)(uintptr_t)lds;
   const bool gather = MODE == BG_WGRAD && p.row_index != nullptr;
-  const int nst = (int)((tl.K + BK - 1) / BK);
   // gathered wgrad: DMA of the row indices of stage s into this wave's ring
   const uint32_t ring = NB * STAGE + (uint32_t)w * 8 * 256;
   auto issue_index = [&](int s) {
@@ -270,8 +272,30 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
   // Epilogue through LDS, slab by slab, in a region of this wave's own: 16
   // bytes a lane and whole row segments per store instruction.
   constexpr int RS = 128 * TN + 32;  // bytes of an LDS row (the pad parts the lane halves' banks)
-  static_assert(4 * 32 * RS <= bg_lds<TM, TN>(), "epilogue fits the ring");
-  float* t = reinterpret_cast<float*>(lds + w * 32 * RS);
+  constexpr int SUMS = (KG - 1) * 4 * VS * TN * 16 * 64 * 4;  // the other groups' accumulators
+  static_assert(SUMS + 4 * 32 * RS <= (KG > 1 ? 160 * 1024 : bg_lds<TM, TN>()), "epilogue fits the ring");
+  if constexpr (KG > 1) {
+    float* sums = reinterpret_cast<float*>(block_lds);
+#pragma unroll
+    for (int i = 0; i < VS; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (grp > 0) sums[((((grp - 1) * 4 + w) * VS * TN + i * TN + j) * 16 + r) * 64 + lane] = acc[i][j][r];
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+      for (int i = 0; i < VS; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            acc[i][j][r] += sums[(((q * 4 + w) * VS * TN + i * TN + j) * 16 + r) * 64 + lane];
+  }
+  float* t = reinterpret_cast<float*>(block_lds + SUMS + w * 32 * RS);
   const int64_t N = MODE == BG_FORWARD ? p.n : p.k;
   const int es = p.y_bf ? 2 : 4;
   const int64_t out_row = MODE == BG_WGRAD ? (int64_t)tl.g * p.n + tl.m0 : tl.row_lo;  // of the tile's first row
@@ -336,7 +360,8 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
 // so that neighbours share operand panels in its L2 and the eighths cost
 // alike.  Light tiles stream weights and heavy ones keep the MFMAs busy: the
 // light ones are mixed evenly among the heavy ones, but for an eighth of all
-// tiles kept for the end, where short tiles level the finish.  An expert's
+// tiles kept for the end, where short tiles level the finish (32768 rows over
+// 128 Zipf experts, n = 1536, k = 2048: 299 us; heavy ones first 324).  An expert's
 // heavy tiles go in bands of 4 m-tiles.  Every wave derives this from the
 // device offsets by wave scans in registers (G experts in NSEG segments of
 // 64 lanes).  False: no tile (block-uniform).
@@ -413,28 +438,87 @@ __device__ __forceinline__ bool bg_schedule(const int32_t* offsets, int G, int64
   return out.row_lo < out.row_hi;
 }
 
-template <int MODE, int TM, int TN, int BK>
-__global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void bf16_tile_kernel(Bf16Args p) {
+// wgrad: the block's expert and tile (index within the expert's `tiles`).
+// Tiles of experts with more than 128 rows multiply, the others mostly write
+// their dW.  The long ones go first, so that the short ones level the finish
+// (32768 rows over 128 Zipf experts, n = 1536, k = 2048, fp32, inputs changing
+// from call to call: 445 us; short ones first 478, mixed evenly 545: the
+// writes push the panels that an expert's tiles share out of the L2s; in
+// expert order 513).  XCD x takes every eighth tile of both lists, so that an
+// expert's tiles of one block of X columns share an L2 where the columns
+// come in eighths.
+template <int NSEG>
+__device__ __forceinline__ bool bg_schedule_wgrad(const int32_t* offsets, int G, int64_t m_total, int tiles, int lane,
+                                                  int64_t& row_lo, int64_t& row_hi, int& g, int& tile) {
+  const int32_t mt = (int32_t)m_total;
+  int32_t lo[NSEG], hi[NSEG], eh[NSEG];
+#pragma unroll
+  for (int i = 0; i < NSEG; ++i)
+    if (64 * i < G) {
+      lo[i] = offsets[min(64 * i + lane, G)];
+      hi[i] = offsets[min(64 * i + lane + 1, G)];
+    }
+  int32_t nh = 0;
+  uint32_t heavy_of = 0;  // bit i: this lane's expert of segment i is heavy
+#pragma unroll
+  for (int i = 0; i < NSEG; ++i) {
+    if (64 * i >= G) continue;
+    lo[i] = min(max(lo[i], 0), mt);
+    hi[i] = min(max(hi[i], lo[i]), mt);
+    const bool h = 64 * i + lane < G && hi[i] - lo[i] > 128;
+    heavy_of |= (uint32_t)h << i;
+    const int32_t incl = wave_incl_scan(h ? 1 : 0);
+    eh[i] = nh + incl - (h ? 1 : 0);  // heavy experts before this one
+    nh += __builtin_amdgcn_readlane(incl, 63);
+  }
+  const int x = (int)(blockIdx.x % 8), j = (int)(blockIdx.x / 8);
+  const int64_t th = (int64_t)nh * tiles, tl = (int64_t)(G - nh) * tiles;
+  const int H = (int)((th - x + 7) / 8), L = (int)((tl - x + 7) / 8);
+  if (j >= H + L) return false;
+  const bool heavy = j < H;
+  const int64_t idx = 8 * (int64_t)(heavy ? j : j - H) + x;
+  const int e = (int)(idx / tiles);  // of the list's experts
+  tile = (int)(idx % tiles);
+  g = 0;
+#pragma unroll
+  for (int i = 0; i < NSEG; ++i) {
+    if (64 * i >= G) continue;
+    const int ex = 64 * i + lane;
+    const bool h = (heavy_of >> i) & 1u;
+    const unsigned long long b = __ballot(ex < G && h == heavy && (h ? eh[i] : ex - eh[i]) == e);
+    if (b) {
+      const int ln = __builtin_ctzll(b);
+      g = 64 * i + ln;
+      row_lo = __builtin_amdgcn_readlane(lo[i], ln);
+      row_hi = __builtin_amdgcn_readlane(hi[i], ln);
+    }
+  }
+  return true;
+}
+
+template <int MODE, int TM, int TN, int BK, int KG>
+__global__ __launch_bounds__(256 * KG, (KG > 1 ? KG : bg_blocks<TM, TN>())) void bf16_tile_kernel(Bf16Args p) {
   typedef BgMode<MODE> M;
   constexpr int BM = 64 * TM, BN = 64 * TN;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds<TM, TN>()];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[KG > 1 ? 160 * 1024 : bg_lds<TM, TN>()];
   constexpr int D = BK / 32, CPR = BK / 8;  // DMAs per slab and wave; chunks of a row operand's LDS row
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = wave & 3, grp = wave >> 2;
   BgTile tl;
   BgOperand<TM> oa;
   BgOperand<TN> ob;
   int vs;
   if constexpr (MODE == BG_WGRAD) {
-    // tiles of an expert one after another, its X columns fastest
+    // an expert's tiles: X columns fastest
     const int tn = (int)((p.n + BM - 1) / BM), tk = (int)((p.k + BN - 1) / BN);
-    const int g = (int)(blockIdx.x / (unsigned)(tn * tk)), r = (int)(blockIdx.x % (unsigned)(tn * tk));
-    const int64_t mt = p.m_total;
-    const int64_t lo = min((int64_t)max(p.offsets[g], 0), mt), hi = min(max((int64_t)p.offsets[g + 1], lo), mt);
-    tl.g = g;
-    tl.row_lo = lo;
-    tl.row_hi = hi;
-    tl.K = hi - lo;
-    tl.m0 = (int64_t)(r / tk) * BM;      // column of dY
+    int r;
+    const bool some = p.groups <= 256
+        ? bg_schedule_wgrad<4>(p.offsets, p.groups, p.m_total, tn * tk, lane, tl.row_lo, tl.row_hi, tl.g, r)
+        : bg_schedule_wgrad<16>(p.offsets, p.groups, p.m_total, tn * tk, lane, tl.row_lo, tl.row_hi, tl.g, r);
+    if (!some) return;  // block-uniform
+    const int64_t lo = tl.row_lo;
+    tl.K = tl.row_hi - lo;
+    tl.m0 = (int64_t)(r / tk) * BM;  // column of dY
     tl.n0 = (int64_t)(r % tk) * BN;  // column of X
     vs = (int)min((int64_t)TM, (p.n - tl.m0 + 63) / 64);
     // column operands: DMA i covers the summed rows (4 i + w) (8 / T) ..
@@ -499,38 +583,61 @@ __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void bf16_tile_kernel(B
       }
     }
   }
+  int nst = (int)((tl.K + BK - 1) / BK);
+  if constexpr (KG > 1) {  // this group's range of the sum
+    nst = (nst + KG - 1) / KG;
+    const int64_t start = (int64_t)grp * nst * BK;
+    tl.K = min((int64_t)nst * BK, max((int64_t)0, tl.K - start));
+    if constexpr (M::a_cols) {
+      oa.base += start * oa.stride;
+    } else {
+#pragma unroll
+      for (int i = 0; i < TM * D; ++i)
+        if (oa.voff[i] != BG_OOB) oa.voff[i] += (uint32_t)start * 2;
+    }
+    if constexpr (!M::b_cols) {
+#pragma unroll
+      for (int i = 0; i < TN * D; ++i)
+        if (ob.voff[i] != BG_OOB) ob.voff[i] += (uint32_t)start * 2;
+    } else if (MODE == BG_DGRAD || !p.row_index) {
+      ob.base += start * ob.stride;
+    }
+    if (MODE == BG_WGRAD) tl.row_lo += start;  // the first summed row
+  }
   if constexpr (TM == 4) {
     switch (vs) {
-      case 4: bg_body<MODE, TM, TN, BK, 4>(p, tl, oa, ob, lds, w, lane); break;
-      case 3: bg_body<MODE, TM, TN, BK, 3>(p, tl, oa, ob, lds, w, lane); break;
-      case 2: bg_body<MODE, TM, TN, BK, 2>(p, tl, oa, ob, lds, w, lane); break;
-      default: bg_body<MODE, TM, TN, BK, 1>(p, tl, oa, ob, lds, w, lane); break;
+      case 4: bg_body<MODE, TM, TN, BK, KG, 4>(p, tl, oa, ob, lds, nst, grp, w, lane); break;
+      case 3: bg_body<MODE, TM, TN, BK, KG, 3>(p, tl, oa, ob, lds, nst, grp, w, lane); break;
+      case 2: bg_body<MODE, TM, TN, BK, KG, 2>(p, tl, oa, ob, lds, nst, grp, w, lane); break;
+      default: bg_body<MODE, TM, TN, BK, KG, 1>(p, tl, oa, ob, lds, nst, grp, w, lane); break;
     }
   } else if constexpr (TM == 3) {
-    if (vs == 3) bg_body<MODE, TM, TN, BK, 3>(p, tl, oa, ob, lds, w, lane);
-    else if (vs == 2) bg_body<MODE, TM, TN, BK, 2>(p, tl, oa, ob, lds, w, lane);
-    else bg_body<MODE, TM, TN, BK, 1>(p, tl, oa, ob, lds, w, lane);
+    if (vs == 3) bg_body<MODE, TM, TN, BK, KG, 3>(p, tl, oa, ob, lds, nst, grp, w, lane);
+    else if (vs == 2) bg_body<MODE, TM, TN, BK, KG, 2>(p, tl, oa, ob, lds, nst, grp, w, lane);
+    else bg_body<MODE, TM, TN, BK, KG, 1>(p, tl, oa, ob, lds, nst, grp, w, lane);
   } else if constexpr (TM == 2) {
-    if (vs == 2) bg_body<MODE, TM, TN, BK, 2>(p, tl, oa, ob, lds, w, lane);
-    else bg_body<MODE, TM, TN, BK, 1>(p, tl, oa, ob, lds, w, lane);
+    if (vs == 2) bg_body<MODE, TM, TN, BK, KG, 2>(p, tl, oa, ob, lds, nst, grp, w, lane);
+    else bg_body<MODE, TM, TN, BK, KG, 1>(p, tl, oa, ob, lds, nst, grp, w, lane);
   } else {
-    bg_body<MODE, TM, TN, BK, 1>(p, tl, oa, ob, lds, w, lane);
+    bg_body<MODE, TM, TN, BK, KG, 1>(p, tl, oa, ob, lds, nst, grp, w, lane);
   }
 }
 
-template <int MODE, int TM, int TN, int BK>
+template <int MODE, int TM, int TN, int BK, int KG = 1>
 static void launch_tiles(const Bf16Args& a, hipStream_t str) {
   Bf16Args p = a;
   int64_t blocks;
   if (MODE == BG_WGRAD) {
+    // every XCD's share of the two lists rounded up
     blocks = (int64_t)p.groups * ((p.n + 64 * TM - 1) / (64 * TM)) * ((p.k + 64 * TN - 1) / (64 * TN));
+    blocks = 8 * ((blocks + 7) / 8 + 1);
   } else {
     // at most a partial m-tile per expert that has rows, and an XCD's two
     // ranges each rounded up
     const int64_t mts = (p.m_total + 64 * TM - 1) / (64 * TM) + (p.groups < p.m_total ? p.groups : p.m_total);
     blocks = 8 * ((mts * (((MODE == BG_FORWARD ? p.n : p.k) + 64 * TN - 1) / (64 * TN)) + 7) / 8 + 2);
   }
-  hipLaunchKernelGGL((bf16_tile_kernel<MODE, TM, TN, BK>), dim3((unsigned)blocks), dim3(256), 0, str, p);
+  hipLaunchKernelGGL((bf16_tile_kernel<MODE, TM, TN, BK, KG>), dim3((unsigned)blocks), dim3(256 * KG), 0, str, p);
 }
 
 // Tiles of a call in units of the CUs (an upper estimate: every expert may add
@@ -552,6 +659,10 @@ static void launch_tiles(const Bf16Args& a, hipStream_t str) {
 //  - wgrad: two 256 x 128 tiles a CU: one writes its dW while the other
 //    multiplies (32768 rows over 128 experts, n = 1536, k = 2048, bf16: 354 us
 //    against 432 for 256 x 256).
+//  - few tiles and a long sum: two wave groups of a block halve the chain (64
+//    rows, n = k = 4096: 18.3 us against 21.5; wgrad of 15262 rows over 3
+//    experts, n = 784, k = 104: 71 against 108; four groups gain no more: a
+//    CU's loads bound them).
 template <int MODE>
 static int launch_bf16(const Bf16Args& p, hipStream_t str) {
   const int64_t cus = nvfp4host::num_cus();
@@ -567,15 +678,18 @@ static int launch_bf16(const Bf16Args& p, hipStream_t str) {
     else if (tiles(3, 2) >= cus && rows >= 128) launch_tiles<MODE, 3, 2, 64>(p, str);
     else if (tiles(2, 2) >= 2 * cus) launch_tiles<MODE, 2, 2, 64>(p, str);
     else if (2 * tiles(1, 2) >= cus && rows >= 24) launch_tiles<MODE, 1, 2, 64>(p, str);
+    else if (2 * tiles(1, 1) <= cus && p.k >= 2048) launch_tiles<MODE, 1, 1, 64, 2>(p, str);
     else launch_tiles<MODE, 1, 1, 64>(p, str);
   } else if constexpr (MODE == BG_DGRAD) {
     if (tiles(2, 4) >= cus) launch_tiles<MODE, 2, 4, 32>(p, str);
     else if (2 * tiles(1, 2) >= cus && rows >= 24) launch_tiles<MODE, 1, 2, 64>(p, str);
+    else if (2 * tiles(1, 1) <= cus && p.n >= 2048) launch_tiles<MODE, 1, 1, 64, 2>(p, str);
     else launch_tiles<MODE, 1, 1, 64>(p, str);
   } else {
     if (tiles(4, 2) >= cus) launch_tiles<MODE, 4, 2, 32>(p, str);
     else if (tiles(2, 2) >= cus) launch_tiles<MODE, 2, 2, 64>(p, str);
-    else if (2 * tiles(1, 2) >= cus) launch_tiles<MODE, 1, 2, 64>(p, str);
+    else if (tiles(1, 2) >= cus) launch_tiles<MODE, 1, 2, 64>(p, str);
+    else if (tiles(1, 1) <= cus && rows >= 1024) launch_tiles<MODE, 1, 1, 64, 2>(p, str);
     else launch_tiles<MODE, 1, 1, 64>(p, str);
   }
   return nvfp4host::launch_status();
