@@ -35,37 +35,38 @@ constexpr int COMBINE_CHUNK = 8;  // choices whose rows are loaded together
 template <bool VEC>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs p, int pieces) {
   const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int64_t t = item / pieces;
-  if (t >= p.tokens) return;
-  const int piece = (int)(item % pieces);
-  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int j0 = 0; j0 < p.topk; j0 += COMBINE_CHUNK) {
-    // lane j holds choice j0 + j: its row (-1 when it has none) and weight
-    const bool has = lane < COMBINE_CHUNK && j0 + lane < p.topk;
-    int32_t sl = has ? p.slot_of[t * p.topk + j0 + lane] : -1;
-    if (sl < 0 || sl >= p.y_rows) sl = -1;
-    const float w = has ? (p.weights ? p.weights[t * p.topk + j0 + lane] : 1.0f) : 0.0f;
-    float v[COMBINE_CHUNK][8];
+  const int64_t items = p.tokens * pieces;
+  for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += (int64_t)gridDim.x * 4) {
+    const int64_t t = item / pieces;
+    const int piece = (int)(item % pieces);
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int j0 = 0; j0 < p.topk; j0 += COMBINE_CHUNK) {
+      // lane j holds choice j0 + j: its row (-1 when it has none) and weight
+      const bool has = lane < COMBINE_CHUNK && j0 + lane < p.topk;
+      int32_t sl = has ? p.slot_of[t * p.topk + j0 + lane] : -1;
+      if (sl < 0 || sl >= p.y_rows) sl = -1;
+      const float w = has ? (p.weights ? p.weights[t * p.topk + j0 + lane] : 1.0f) : 0.0f;
+      float v[COMBINE_CHUNK][8];
 #pragma unroll
-    for (int j = 0; j < COMBINE_CHUNK; ++j) {
-      const int32_t row = __builtin_amdgcn_readlane(sl, j);
-      if (row >= 0) {
-        load8<VEC>(row_at(p.y, p.y_bf, row, p.d), p.y_bf, p.d, piece, 64, lane, v[j]);
-      } else {
+      for (int j = 0; j < COMBINE_CHUNK; ++j) {
+        const int32_t row = __builtin_amdgcn_readlane(sl, j);
+        if (row >= 0) {
+          load8<VEC>(row_at(p.y, p.y_bf, row, p.d), p.y_bf, p.d, piece, 64, lane, v[j]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+          for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < COMBINE_CHUNK; ++j) {
+        if (__builtin_amdgcn_readlane(sl, j) < 0) continue;  // nothing added, whatever its weight
+        const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(wj, v[j][i], acc[i]);
       }
     }
-#pragma unroll
-    for (int j = 0; j < COMBINE_CHUNK; ++j) {
-      if (__builtin_amdgcn_readlane(sl, j) < 0) continue;  // nothing added, whatever its weight
-      const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(wj, v[j][i], acc[i]);
-    }
+    store8<VEC>(row_at(p.out, p.o_bf, t, p.d), p.o_bf, p.d, piece, 64, lane, acc);
   }
-  store8<VEC>(row_at(p.out, p.o_bf, t, p.d), p.o_bf, p.d, piece, 64, lane, acc);
 }
 
 template <bool VEC>
@@ -147,13 +148,13 @@ extern "C" int nvfp4_moe_combine(const void* y, int y_type, int64_t y_rows, cons
   if (bad_elem(y, y_type) || bad_elem(out, out_type) || !aligned(slot_of, 4) || !aligned(weights, 4))
     return NVFP4_ERROR_MISALIGNED;
   const int pieces = (int)((d + 511) / 512);
-  if (tokens > (((int64_t)1 << 33) - 4) / pieces) return NVFP4_ERROR_UNSUPPORTED_SHAPE;
   if ((st = nvfp4host::check_arch())) return st;
   nvfp4::CombineArgs p{};
   p.y = y; p.slot_of = slot_of; p.weights = weights; p.out = out;
   p.y_rows = y_rows; p.tokens = tokens; p.d = d; p.topk = (int)topk;
   p.y_bf = y_type == NVFP4_TYPE_BF16; p.o_bf = out_type == NVFP4_TYPE_BF16;
-  const dim3 grid((unsigned)((tokens * pieces + 3) / 4));
+  const int64_t blocks = (tokens * pieces + 3) / 4;
+  const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
   if (nvfp4::combine_vec(d, y, out, nullptr))
     hipLaunchKernelGGL(nvfp4::combine_kernel<true>, grid, dim3(256), 0, (hipStream_t)stream, p, pieces);
   else

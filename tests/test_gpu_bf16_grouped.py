@@ -155,6 +155,27 @@ def test_wgrad_adds_up(out):
     ref.close(got, y, bound, "in place")
 
 
+def test_empty_sums_give_zeros():
+    off = torch.tensor([0, 3, 3, 10], dtype=torch.int32, device=DEV)
+    x, w = torch.empty(12, 0, dtype=BF16, device=DEV), torch.empty(3, 16, 0, dtype=BF16, device=DEV)
+    out = torch.full((12, 16), 5.0, device=DEV)
+    nv.nvfp4_bf16_grouped_gemm(x, off, w, out=out)
+    assert (out[:10] == 0).all() and (out[10:] == 5).all()
+    dy, w = torch.empty(12, 0, dtype=BF16, device=DEV), torch.empty(3, 0, 16, dtype=BF16, device=DEV)
+    out = torch.full((12, 16), 5.0, device=DEV)
+    nv.nvfp4_bf16_grouped_dgrad(dy, off, w, out=out)
+    assert (out[:10] == 0).all() and (out[10:] == 5).all()
+    # nothing to write at all
+    none = torch.empty(0, 16, dtype=BF16, device=DEV)
+    assert nv.nvfp4_bf16_grouped_gemm(none, off, torch.zeros(3, 8, 16, dtype=BF16, device=DEV)).shape == (0, 8)
+    # every index outside an x without rows
+    idx = torch.zeros(12, dtype=torch.int32, device=DEV)
+    got = nv.nvfp4_bf16_grouped_gemm(none, off, torch.ones(3, 8, 16, dtype=BF16, device=DEV), row_index=idx)
+    assert (got[:10] == 0).all()
+    dy = torch.ones(12, 8, dtype=BF16, device=DEV)
+    assert (nv.nvfp4_bf16_grouped_wgrad(dy, none, off, row_index=idx) == 0).all()
+
+
 def test_wgrad_of_no_rows():
     c = case([0, 0], 72, 136, seed=8)
     assert (run("wgrad", c) == 0).all()
@@ -265,3 +286,43 @@ def test_refusals():
     for n, k in ((60, 72), (64, 68)):
         with pytest.raises(nv.NVFP4Error):
             f(torch.zeros(11, k, dtype=BF16, device=DEV), off, torch.zeros(2, n, k, dtype=BF16, device=DEV))
+
+
+# (way, counts, n, k): layouts that reach every tile shape the calls choose
+# from on 256 CUs, ragged in rows, columns and the summed dimension
+SHAPES = {
+    "forward 256x256": ("forward", [1000, 0, 1700, 396, 1000], 12296, 72),
+    "forward 192x128": ("forward", [700, 64, 193, 1091], 2440, 200),
+    "forward 128x128": ("forward", [7, 30, 0, 1] * 16, 1032, 136),
+    "forward 64x128": ("forward", [130, 64, 1, 40], 1800, 264),
+    "forward 64x64": ("forward", [3, 0, 5, 1], 1032, 264),
+    "forward 64x64 split": ("forward", [3, 0, 70], 264, 2312),
+    "dgrad 128x256": ("dgrad", [300, 129, 0, 128, 1], 136, 8200),
+    "dgrad 64x128": ("dgrad", [130, 64, 1, 40], 264, 1800),
+    "dgrad 64x64": ("dgrad", [3, 0, 5, 1], 264, 1032),
+    "dgrad 64x64 split": ("dgrad", [3, 0, 70], 2312, 264),
+    "wgrad 256x128": ("wgrad", [140, 0, 1, 33, 257, 64, 128, 129], 1000, 1032),
+    "wgrad 128x128": ("wgrad", [140, 0, 1, 33, 257, 64, 128, 129], 520, 1032),
+    "wgrad 64x128": ("wgrad", [140, 0, 1, 33], 520, 1032),
+    "wgrad 64x64": ("wgrad", [140, 0, 1, 33], 136, 1032),
+    "wgrad 64x64 split": ("wgrad", [3000, 0, 130, 1500], 136, 264),
+}
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_every_tile_shape(shape, out):
+    way, counts, n, k = SHAPES[shape]
+    c = case(counts, n, k, tokens=0 if way == "dgrad" else 333, seed=n)
+    if c["index"] is not None:
+        c["index"][::7] = -1
+    got = run(way, c, out_dtype=out)
+    ref.close(got, *want(way, c), shape)
+    assert torch.equal(run(way, c, out_dtype=out), got)
+
+
+@pytest.mark.parametrize("shape", [s for s in SHAPES if not s.startswith("dgrad")])
+def test_every_tile_shape_in_place_rows(shape):
+    way, counts, n, k = SHAPES[shape]
+    c = case(counts, n, k, seed=k)
+    ref.close(run(way, c), *want(way, c), shape)

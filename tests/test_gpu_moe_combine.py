@@ -58,9 +58,18 @@ def test_types(y, out, dy):
         check(c, out, dy, weights=False)
 
 
-@pytest.mark.parametrize("tokens", [1, 2, 63, 1000, 20000])
-def test_token_counts(tokens):
-    check(make(tokens, 2, 72, extra=3, seed=tokens))
+@pytest.mark.parametrize("tokens,topk,d", [(1, 2, 72), (2, 2, 72), (63, 2, 72), (1000, 2, 72), (20000, 2, 72), (2_200_000, 1, 1030)],
+                         ids=lambda v: str(v))
+def test_token_counts(tokens, topk, d):
+    if tokens > 10 ** 6:  # more pieces than a launch has blocks, and offsets past 4 GiB
+        y = (torch.arange(tokens, device=DEV) % 251).to(BF16)[:, None].expand(tokens, d).contiguous()
+        slot = torch.arange(tokens, device=DEV, dtype=torch.int32).flip(0)[:, None].contiguous()
+        got = nv.nvfp4_moe_combine(y, slot)
+        assert torch.equal(got, y.flip(0))
+        back = nv.nvfp4_moe_combine_backward(got, y, slot)
+        assert torch.equal(back["dy"], y)
+        return
+    check(make(tokens, topk, d, extra=3, seed=tokens))
 
 
 def test_slots_outside_and_rows_unnamed():
