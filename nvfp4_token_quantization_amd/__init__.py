@@ -910,10 +910,11 @@ def nvfp4_clip_grad_norm(grads, max_norm, out=None, norm_only=False, workspace=N
         raise ValueError("grads must hold at least one tensor")
     dev = grads[0].device if isinstance(grads[0], torch.Tensor) else None
     types, counts, ptrs = [], [], []
-    for i, t in enumerate(grads):
-        _dev(t, "a gradient", _FLOATS)
+    for t in grads:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in _TYPES and t.is_contiguous()):
+            _dev(t, "a gradient", _FLOATS)  # raises
         if t.device != dev:
-            raise ValueError("grads[%d] must be on %s (got %s)" % (i, dev, t.device))
+            raise ValueError("every gradient must be on %s (got %s)" % (dev, t.device))
         types.append(_TYPES[t.dtype])
         counts.append(t.numel())
         ptrs.append(t.data_ptr())
@@ -927,11 +928,12 @@ def nvfp4_clip_grad_norm(grads, max_norm, out=None, norm_only=False, workspace=N
         if len(out) != n:
             raise ValueError("out must have one tensor per gradient")
         outs = []
-        for i, (t, g) in enumerate(zip(out, grads)):
-            _dev(t, "an out tensor", (g.dtype,))
+        for t, g in zip(out, grads):
+            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == g.dtype and t.is_contiguous()):
+                _dev(t, "an out tensor", (g.dtype,))  # raises
             if t.shape != g.shape or t.device != dev:
-                raise ValueError("out[%d] must have shape %s on %s (got %s on %s)" % (i, tuple(g.shape), dev,
-                                                                                     tuple(t.shape), t.device))
+                raise ValueError("an out tensor must have its gradient's shape %s on %s (got %s on %s)" % (
+                    tuple(g.shape), dev, tuple(t.shape), t.device))
             outs.append(t.data_ptr())
     if outs is not None:
         _disjoint(ptrs, outs, [c * (2 if k else 4) for c, k in zip(counts, types)])
