@@ -28,8 +28,9 @@
  *   blocks along K), Y fp32 [m, n] row-major.
  *
  * Conventions for every call:
- *   - Pointers are device pointers owned by the caller.  The library never
- *     allocates, frees or keeps them.  Inputs are read-only; outputs are
+ *   - Pointers are device pointers owned by the caller (host arrays where a
+ *     call says so).  The library never allocates, frees or keeps them; calls
+ *     that need a workspace take the caller's and say how large.  Inputs are read-only; outputs are
  *     overwritten; inputs and outputs must not overlap.
  *   - `stream` is a hipStream_t passed as void* (NULL = default stream).
  *     Calls are asynchronous and never synchronize the host.  The host never
@@ -43,8 +44,8 @@
  *   - GEMM sizes: besides each call's own limits, an output whose tile grid
  *     ((m_total / 128 + groups + 1) x (n / 64 + 1)) passes 2^28 tiles -- far
  *     beyond device memory -- is rejected with UNSUPPORTED_SHAPE.
- *   - Inputs must be finite; non-finite bf16 inputs give unspecified codes
- *     (no fault).  Stateless and re-entrant; calls on one stream are ordered.
+ *   - Inputs of the quantizing calls must be finite; non-finite bf16 inputs
+ *     give unspecified codes (no fault).  Stateless and re-entrant; calls on one stream are ordered.
  *   - Device-side preconditions (values in device memory, which the host
  *     never reads) are undefined when violated, never a fault: non-finite
  *     bf16 / f32 inputs, supplied amax or scales (a supplied amax also < 0),
@@ -452,9 +453,9 @@ int nvfp4_bf16_grouped_wgrad(const uint16_t* dy, int64_t m_total, const uint16_t
  *   r' = residual + scale * gate * n                  (rounded to its type)
  *   h  = bf16(r' / sqrt(mean(r'^2) + eps) * norm_weight)
  *
- * Defined by: the miniTE page, section Transformer Engine路径优化 (amax reuse
- * and fusion around the low-precision GEMMs): the rows that are quantized
- * come out of a norm, as those of nvfp4_swiglu_quantize_rows out of SwiGLU.
+ * The rows that the layers' quantizers read come out of a norm, as those of
+ * nvfp4_swiglu_quantize_rows come out of SwiGLU.  The pages describe no norm:
+ * the formulas above are the definition.
  *
  *   x         [rows, d] block output b (fp32 as the GEMMs write it, or bf16).
  *   residual  NULL (zeros) or [rows, d]; residual_out NULL or [rows, d] of
@@ -509,8 +510,8 @@ int nvfp4_residual_norm_backward(const void* x, int x_type, const void* residual
  *   dy[slot_of[t, j]] = weights[t, j] * dout[t]
  *   d_weights[t, j]   = <dout[t], y[slot_of[t, j]]>
  *
- * Defined by: the miniTE page, section Transformer Engine路径优化 (contiguous
- * layouts: the routed rows of the grouped GEMMs go back to their tokens).
+ * The way back from the contiguous per-expert layout (the miniTE page, section
+ * Transformer Engine路径优化) to the tokens.
  *
  *   y [y_rows, d], dout / out [tokens, d], dy [y_rows, d]: fp32 or bf16 each.
  *   slot_of [tokens, topk] i32: a slot outside [0, y_rows) adds nothing and
@@ -538,8 +539,9 @@ int nvfp4_moe_combine_backward(const void* dout, int dout_type, const void* y, i
  *   norm = sqrt(sum over tensors of sum g^2)
  *   out  = round(g * min(1, max_norm / (norm + 1e-6)))   in g's own type
  *
- * Defined by: the learner update of the TRIAGE page, section 核心方法; its
- * gradients are what nvfp4_bf16_grouped_wgrad and the dense layers write.
+ * For a learner's update from the gradients that nvfp4_bf16_grouped_wgrad and
+ * the dense layers write.  The pages describe no clipping: the formulas above
+ * are the definition.
  *
  *   grads, out, counts, types: HOST arrays of `tensors` entries, read during
  *   the call (device pointers of the tensors, elements, NVFP4_TYPE_*); out

@@ -4,6 +4,13 @@
 //   forward  Y[i]  = X[r(i)] W_e^T      rows i of expert e, r(i) = row_index[i] or i
 //   dgrad    dX[i] = dY[i] W_e
 //   wgrad    dW_e  = add_e + sum_{i of e} dY[i]^T X[r(i)]
+//
+// bf16 products are exact in fp32 and summed there by the MFMAs; an output is
+// rounded once.  One expert of 8192 rows, n = k = 8192 (bf16 output): forward
+// 1298 TFLOP/s, dgrad 1196, wgrad 1190, where a large library product
+// reaches 1377.  Ragged layouts are bound by HBM and by padding to 64-row
+// slabs: 32768 rows over 128 Zipf experts, n = 1536, k = 2048, fp32 output: 302
+// us forward (3.3 TB/s of its bytes, 682 TFLOP/s), 446 us wgrad (3.9 TB/s).
 #include "gemm_common.h"
 #include "rowwise.h"
 
@@ -29,19 +36,22 @@ struct Bf16Args {
 // slabs 2 i + wr, so that a ragged tile's empty slabs fall on both wave rows
 // alike and are left out in pairs (VS <= TM pairs hold rows).
 //
-// A stage is 32 elements of the summed dimension of both operands, brought
-// to LDS by DMA (buffer_load ... lds, 1 KiB an instruction) into a ring of
-// four stage buffers: the DMA of stage s + 4 goes out when every wave has
-// read stage s, three stages ahead of its use.  Two layouts:
+// A stage is BK = 32 or 64 elements of the summed dimension of both operands,
+// brought to LDS by DMA (buffer_load ... lds, 1 KiB an instruction) into a
+// ring of NB stage buffers: the DMA of stage s + NB goes out when every wave
+// has read stage s, NB - 1 stages ahead of its use.  Two layouts:
 //   row operands (X, dY and W of the forward product, dY of dgrad), whose
-//     summed dimension is contiguous: LDS rows of 64 bytes, one per output
-//     row or column, their 16-byte chunks XOR-swizzled by lds_swz, read 8
-//     summed elements a lane with ds_read_b128;
+//     summed dimension is contiguous: LDS rows of BK elements, one per output
+//     row or column, their 16-byte chunks XOR-swizzled by bg_row_swz, read 8
+//     summed elements a lane with ds_read_b128.  BK = 64 takes whole 128-byte
+//     lines (forward, 8192 cubed, 256 x 256: 840 us against 858 with 32);
 //   column operands (W of dgrad, dY and X of wgrad), whose output dimension
-//     is contiguous: 32 LDS rows, one per summed index, read with
+//     is contiguous: BK LDS rows, one per summed index, read with
 //     ds_read_b64_tr_b16, which hands each lane 4 summed elements of its
 //     column.  Chunks are XOR-swizzled by row so that the four rows of 16
 //     lanes (and of 32) lie in different banks.
+// Neither layout shows bank conflicts in the counters (SQ_LDS_BANK_CONFLICT 0;
+// 4% of the LDS cycles of the row reads beside column reads in dgrad).
 // Rows, columns and summed elements that do not exist get an offset past the
 // resource, for which the DMA writes zeros.
 constexpr uint32_t BG_OOB = 0x80000000u;
