@@ -479,8 +479,8 @@ int nvfp4_bf16_grouped_wgrad(const uint16_t* dy, int64_t m_total, const uint16_t
  *   d_post_weight, d_gate, d_norm_weight may be NULL.
  *   d_residual_out and d_residual have residual_type and may be one buffer.
  *   Column sums are added in a fixed order (no atomics).  workspace: at least
- *   nvfp4_residual_norm_backward_workspace(rows, d) bytes of the caller's,
- *   16-byte aligned, free for other use when the call's work has completed;
+ *   nvfp4_residual_norm_backward_workspace(rows, d) bytes (it depends on the
+ *   current device's number of CUs) of the caller's, 16-byte aligned, free for other use when the call's work has completed;
  *   needed when one of the [d] gradients is asked for.  rows == 0 gives zero
  *   column sums.
  * Errors: INVALID_VALUE (sizes, types, eps, a missing or too small workspace,
@@ -518,8 +518,8 @@ int nvfp4_residual_norm_backward(const void* x, int x_type, const void* residual
  *   gets no gradient (d_weights 0).  weights NULL (ones) or [tokens, topk]
  *   f32.  dy and d_weights: either may be NULL, y too without d_weights.
  * Forward: a row may be named by many slots.  Backward: no row may be named
- * twice in one call (as in a routing's slot_of); its dy is then that of one
- * of them.  Rows of dy that no slot names are not written.  Sums in fp32, in
+ * twice in one call (as in a routing's slot_of, where none is); the dy of
+ * such a row is unspecified.  Rows of dy that no slot names are not written.  Sums in fp32, in
  * order j (dot products in a fixed order).  1 <= topk <= 64, d <= 2^24,
  * tokens * topk <= 2^31.
  * Errors: INVALID_VALUE, UNSUPPORTED_SHAPE, MISALIGNED (elements to their

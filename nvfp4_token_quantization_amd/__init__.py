@@ -809,8 +809,9 @@ def nvfp4_residual_norm_backward(x, residual, norm_weight=None, dh=None, d_resid
         same = key == "d_residual" and d_residual is not None and t.data_ptr() == d_residual.data_ptr()
         _no_overlap(t, "out " + key, x, residual, dh, None if same else d_residual, post_weight, gate, norm_weight)
     g = res.get
-    need = lib().nvfp4_residual_norm_backward_workspace(rows, d)
     if workspace is None:
+        with _on(dev):
+            need = lib().nvfp4_residual_norm_backward_workspace(rows, d)
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     else:
         _dev(workspace, "workspace", (torch.uint8,), 1)

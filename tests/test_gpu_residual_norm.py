@@ -152,6 +152,35 @@ def test_rows_do_not_depend_on_the_batch():
         assert torch.equal(few[key], whole[key][1234:1241])
 
 
+def test_offsets_past_32_bits():
+    """Rows beyond 4 GiB of each operand have the bits they have on their own."""
+    rows, d = 1_060_000, 1024
+    c = make(8, d, seed=3)
+    x = torch.empty(rows, d, dtype=F32, device=DEV)
+    r = torch.empty(rows, d, dtype=F32, device=DEV)
+    x[-8:], r[-8:] = c["x"], c["residual"].float()
+    x[:-8] = 1.0
+    r[:-8] = 0.5
+    few = dict(c, x=x[-8:].clone(), residual=r[-8:].clone())
+    want = forward(few)
+    got = forward(dict(c, x=x, residual=r), out={"residual": r})
+    for key in want:
+        assert torch.equal(got[key][-8:], want[key])
+    dh = torch.zeros(rows, d, dtype=BF16, device=DEV)
+    dr = torch.zeros(rows, d, dtype=F32, device=DEV)
+    dh[-8:], dr[-8:] = c["dh"], c["dr"].float()
+    few.update(dh=dh[-8:].clone(), dr=dr[-8:].clone())
+    want = backward(few, want["residual"])
+    got = backward(dict(c, x=x, dh=dh, dr=dr), r, out={"d_residual": dr})
+    for key in ("dx", "d_residual"):
+        assert torch.equal(got[key][-8:], want[key])
+    # the other rows' gradients are zero, so the column sums are the few rows', added in another order
+    for key, (w, bound) in ref.norm_backward(few["x"], r[-8:], c["norm_weight"], few["dh"], few["dr"], c["post_weight"],
+                                             c["gate"], 0.7, EPS).items():
+        if key in ("d_post_weight", "d_norm_weight", "d_gate"):
+            ref.close(got[key], w, bound, key)
+
+
 def test_in_place_and_unaligned_rows():
     c = make(50, 520)
     want = forward(c)
