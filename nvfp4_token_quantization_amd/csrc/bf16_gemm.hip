@@ -248,19 +248,25 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
     for (int k = 0; k < NC; ++k) issue_one(q, idx, k);
     if (gather) issue_index(s + NB);
   }
-  bf16x8 fa[2][VS], fb[2][TN];
+  // Fragments are read LOOK MFMA steps ahead: two where a step has few MFMAs,
+  // which would not cover the LDS latency.
+  constexpr int LOOK = VS <= 2 && NT == 4 ? 2 : 1, FB = 2 * LOOK;
+  bf16x8 fa[FB][VS], fb[FB][TN];
   if (gather) wait_vmcnt<(NB - 1) * (NC + 1)>();
   else wait_vmcnt<(NB - 1) * NC>();
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
-  for (int k = 0; k < VS + TN; ++k) read_one(0, 0, fa[0], fb[0], k);
+  for (int t = 0; t < LOOK; ++t)
+#pragma unroll
+    for (int k = 0; k < VS + TN; ++k) read_one(0, t, fa[t], fb[t], k);
   int cur = 0;
   for (int s = 0; s < nst; ++s) {
     const int nxt = cur + 1 == NB ? 0 : cur + 1;
     if (gather) gather_rows(s + NB, idx);
 #pragma unroll
-    for (int t = 0; t + 1 < NT; ++t)
-      mma(fa[t & 1], fb[t & 1], VS + TN, [&](int k) { read_one(cur, t + 1, fa[(t + 1) & 1], fb[(t + 1) & 1], k); });
+    for (int t = 0; t < NT - LOOK; ++t)
+      mma(fa[t % FB], fb[t % FB], VS + TN,
+          [&](int k) { read_one(cur, t + LOOK, fa[(t + LOOK) % FB], fb[(t + LOOK) % FB], k); });
     // every read of stage s has landed and stage s + 1 is there: after the
     // barrier, for all four waves
     wait_lgkmcnt0();
@@ -268,10 +274,14 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
     else wait_vmcnt<(NB - 2) * NC>();
     asm volatile("s_barrier" ::: "memory");
     const Issue q = issue_at(s + NB, cur);
-    mma(fa[1], fb[1], VS + TN + NC, [&](int k) {
-      if (k < VS + TN) read_one(nxt, 0, fa[0], fb[0], k);
-      else issue_one(q, idx, k - VS - TN);
-    });
+#pragma unroll
+    for (int u = 0; u < LOOK; ++u) {
+      const int t = NT - LOOK + u, d0 = NC * u / LOOK, d1 = NC * (u + 1) / LOOK;
+      mma(fa[t % FB], fb[t % FB], VS + TN + d1 - d0, [&](int k) {
+        if (k < VS + TN) read_one(nxt, u, fa[u], fb[u], k);
+        else issue_one(q, idx, d0 + k - VS - TN);
+      });
+    }
     if (gather) issue_index(s + 2 * NB);
     cur = nxt;
   }
@@ -668,7 +678,10 @@ static void launch_tiles(const Bf16Args& a, hipStream_t str) {
 //    (32768 rows over 128 experts, n = 2048, k = 768: 165 us against 189).
 //  - wgrad: two 256 x 128 tiles a CU: one writes its dW while the other
 //    multiplies (32768 rows over 128 experts, n = 1536, k = 2048, bf16: 354 us
-//    against 432 for 256 x 256).
+//    against 432 for 256 x 256); with one tile a CU and long sums, smaller
+//    tiles lose nothing where experts have equal rows and spread the largest
+//    one's work where they do not (32768 rows over 8 Zipf experts, n = k =
+//    1024: 128 x 128 192 us against 244; equal experts 93 and 92).
 //  - few tiles and a long sum: two wave groups of a block halve the chain (64
 //    rows, n = k = 4096: 18.3 us against 21.5; wgrad of 15262 rows over 3
 //    experts, n = 784, k = 104: 71 against 108; four groups gain no more: a
@@ -696,7 +709,7 @@ static int launch_bf16(const Bf16Args& p, hipStream_t str) {
     else if (2 * tiles(1, 1) <= cus && p.n >= 2048) launch_tiles<MODE, 1, 1, 64, 2>(p, str);
     else launch_tiles<MODE, 1, 1, 64>(p, str);
   } else {
-    if (tiles(4, 2) >= cus) launch_tiles<MODE, 4, 2, 32>(p, str);
+    if (tiles(4, 2) >= (rows < 1024 ? cus : 2 * cus)) launch_tiles<MODE, 4, 2, 32>(p, str);
     else if (tiles(2, 2) >= cus) launch_tiles<MODE, 2, 2, 64>(p, str);
     else if (tiles(1, 2) >= cus) launch_tiles<MODE, 1, 2, 64>(p, str);
     else if (tiles(1, 1) <= cus && rows >= 1024) launch_tiles<MODE, 1, 1, 64, 2>(p, str);
