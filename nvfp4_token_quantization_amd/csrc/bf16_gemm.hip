@@ -11,6 +11,8 @@
 // reaches 1377.  Ragged layouts are bound by HBM and by padding to 64-row
 // slabs: 32768 rows over 128 Zipf experts, n = 1536, k = 2048, fp32 output: 302
 // us forward (3.3 TB/s of its bytes, 682 TFLOP/s), 446 us wgrad (3.9 TB/s).
+#include <type_traits>
+
 #include "gemm_common.h"
 #include "rowwise.h"
 
@@ -327,50 +329,57 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
   const __amdgpu_buffer_rsrc_t radd =
       out_rsrc(reinterpret_cast<float*>(const_cast<uint8_t*>(static_cast<const uint8_t*>(p.add)) + (p.add ? out_row * N * es : 0)),
                p.add ? rows * N * es : 0);
+  // pieces of 16 bytes a lane: columns of a piece, lanes a row, pieces a slab
+  auto slab = [&](auto bf, int i, int r0) {
+    constexpr bool BF = decltype(bf)::value;
+    constexpr int CPP = BF ? 8 : 4, LPR = 32 * TN / CPP, U = 32 * LPR / 64;
+    const int64_t col = col0 + CPP * (lane % LPR);
+    uint32_t off[U];
+    u32x4 av[U];
 #pragma unroll
-  for (int i = 0; i < VS; ++i) {
-    const int r0 = 32 * (2 * i + wr);
+    for (int u = 0; u < U; ++u) {
+      const int r = u * (64 / LPR) + lane / LPR;
+      off[u] = col < N ? (uint32_t)(r0 + r) * nb + (uint32_t)col * (BF ? 2 : 4) : BG_OOB;
+      // all of the slab's addends before its first store: add may be y itself,
+      // and one load after another would wait for memory U times
+      if (MODE == BG_WGRAD && p.add) av[u] = __builtin_amdgcn_raw_buffer_load_b128(radd, off[u], 0, 0);
+    }
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         t[((8 * (r >> 2) + 4 * h + (r & 3)) * RS + (32 * j + li) * 4) / 4] = acc[i][j][r];
     wave_lds_sync();
-    if (p.y_bf) {
-      constexpr int LPR = 4 * TN;  // lanes a row, 8 columns each
-      const int64_t col = col0 + 8 * (lane % LPR);
 #pragma unroll
-      for (int u = 0; u < 32 * LPR / 64; ++u) {
-        const int r = u * (64 / LPR) + lane / LPR;
-        const f32x4* q = reinterpret_cast<const f32x4*>(reinterpret_cast<const uint8_t*>(t) + r * RS + (lane % LPR) * 32);
+    for (int u = 0; u < U; ++u) {
+      const int r = u * (64 / LPR) + lane / LPR;
+      const f32x4* q = reinterpret_cast<const f32x4*>(reinterpret_cast<const uint8_t*>(t) + r * RS + (lane % LPR) * 4 * CPP);
+      u32x4 o;
+      if (BF) {
         f32x4 a = q[0], b = q[1];
-        const uint32_t off = col < N ? (uint32_t)(r0 + r) * nb + (uint32_t)col * 2 : BG_OOB;
         if (MODE == BG_WGRAD && p.add) {
-          const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(radd, off, 0, 0);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            a[2 * c] += __uint_as_float(v[c] << 16);
-            a[2 * c + 1] += __uint_as_float(v[c] & 0xFFFF0000u);
-            b[2 * c] += __uint_as_float(v[2 + c] << 16);
-            b[2 * c + 1] += __uint_as_float(v[2 + c] & 0xFFFF0000u);
+            a[2 * c] += __uint_as_float(av[u][c] << 16);
+            a[2 * c + 1] += __uint_as_float(av[u][c] & 0xFFFF0000u);
+            b[2 * c] += __uint_as_float(av[u][2 + c] << 16);
+            b[2 * c + 1] += __uint_as_float(av[u][2 + c] & 0xFFFF0000u);
           }
         }
-        const u32x4 o = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
-        __builtin_amdgcn_raw_buffer_store_b128(o, ry, off, 0, 2);
+        o = (u32x4){pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
+      } else {
+        f32x4 a = q[0];
+        if (MODE == BG_WGRAD && p.add) a += __builtin_bit_cast(f32x4, av[u]);
+        o = __builtin_bit_cast(u32x4, a);
       }
-    } else {
-      constexpr int LPR = 8 * TN;  // lanes a row, 4 columns each
-      const int64_t col = col0 + 4 * (lane % LPR);
-#pragma unroll
-      for (int u = 0; u < 32 * LPR / 64; ++u) {
-        const int r = u * (64 / LPR) + lane / LPR;
-        f32x4 a = *reinterpret_cast<const f32x4*>(reinterpret_cast<const uint8_t*>(t) + r * RS + (lane % LPR) * 16);
-        const uint32_t off = col < N ? (uint32_t)(r0 + r) * nb + (uint32_t)col * 4 : BG_OOB;
-        if (MODE == BG_WGRAD && p.add) a += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(radd, off, 0, 0));
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, a), ry, off, 0, 2);
-      }
+      __builtin_amdgcn_raw_buffer_store_b128(o, ry, off[u], 0, 2);
     }
     wave_lds_sync();
+  };
+#pragma unroll
+  for (int i = 0; i < VS; ++i) {
+    if (p.y_bf) slab(std::true_type{}, i, 32 * (2 * i + wr));
+    else slab(std::false_type{}, i, 32 * (2 * i + wr));
   }
 }
 
