@@ -223,9 +223,9 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
   for (int i = 0; i < VS; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = (f32x16){0};
-  // The MFMAs of one half stage with `items` other instructions spread among
-  // them, pinned in this order: the matrix pipe never waits for a burst of
-  // LDS reads or DMAs to issue.
+  // The MFMAs of one step with `items` other instructions spread among them,
+  // pinned in this order: the matrix pipe never waits for a burst of LDS
+  // reads or DMAs to issue.
   auto mma = [&](const bf16x8 (&fa)[VS], const bf16x8 (&fb)[TN], int items, auto&& item) {
     constexpr int S = VS * TN;
 #pragma unroll
@@ -390,10 +390,10 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
 // alike.  Light tiles stream weights and heavy ones keep the MFMAs busy: the
 // light ones are mixed evenly among the heavy ones, but for an eighth of all
 // tiles kept for the end, where short tiles level the finish (32768 rows over
-// 128 Zipf experts, n = 1536, k = 2048: 299 us; heavy ones first 324).  An expert's
-// heavy tiles go in bands of 4 m-tiles.  Every wave derives this from the
-// device offsets by wave scans in registers (G experts in NSEG segments of
-// 64 lanes).  False: no tile (block-uniform).
+// 128 Zipf experts, n = 1536, k = 2048: 299 us; heavy ones first 324).  An
+// expert's heavy tiles go in bands of 4 m-tiles.  Every wave derives this from
+// the device offsets by wave scans in registers (G experts in NSEG segments
+// of 64 lanes).  False: no tile (block-uniform).
 template <int NSEG, int TM, int TN>
 __device__ __forceinline__ bool bg_schedule(const int32_t* offsets, int G, int64_t m_total, int tn, int lane, TileRange& out) {
   constexpr int BM = 64 * TM;
@@ -440,7 +440,7 @@ __device__ __forceinline__ bool bg_schedule(const int32_t* offsets, int G, int64
 #pragma unroll
   for (int i = 0; i < NSEG; ++i)
     if (64 * i < G) count += __popcll(__ballot((heavy ? eh[i] : el[i]) <= m));
-  const int g = count - 1, ln = g & 63;
+  const int g = max(count - 1, 0), ln = g & 63;
   int32_t lo_s = lo[0], hi_s = hi[0], eh_s = eh[0];
 #pragma unroll
   for (int i = 1; i < NSEG; ++i)
@@ -452,6 +452,7 @@ __device__ __forceinline__ bool bg_schedule(const int32_t* offsets, int G, int64
     const int32_t slabs = (rhi - rlo) / 64 + ((rhi - rlo) % 64 != 0);
     const int mts = slabs / TM + (2 * (slabs % TM) > TM);
     const int q = idx - e0 * tn;  // within the expert's mts x tn heavy tiles
+    if (q < 0 || q >= mts * tn) return false;  // never for non-decreasing offsets
     const int band = q / (4 * tn), within = q % (4 * tn), bh = min(4, mts - 4 * band);
     m = 4 * band + within % bh;
     n = within / bh;
@@ -509,6 +510,7 @@ __device__ __forceinline__ bool bg_schedule_wgrad(const int32_t* offsets, int G,
   const int e = (int)(idx / tiles);  // of the list's experts
   tile = (int)(idx % tiles);
   g = 0;
+  row_lo = row_hi = 0;
 #pragma unroll
   for (int i = 0; i < NSEG; ++i) {
     if (64 * i >= G) continue;

@@ -294,11 +294,11 @@ SHAPES = {
     "forward 256x256": ("forward", [1000, 0, 1700, 396, 1000], 12296, 72),
     "forward 192x128": ("forward", [700, 64, 193, 1091], 2440, 200),
     "forward 128x128": ("forward", [7, 30, 0, 1] * 16, 1032, 136),
-    "forward 64x128": ("forward", [130, 64, 1, 40], 1800, 264),
+    "forward 64x128": ("forward", [130, 64, 1, 40], 2440, 264),
     "forward 64x64": ("forward", [3, 0, 5, 1], 1032, 264),
     "forward 64x64 split": ("forward", [3, 0, 70], 264, 2312),
     "dgrad 128x256": ("dgrad", [300, 129, 0, 128, 1], 136, 8200),
-    "dgrad 64x128": ("dgrad", [130, 64, 1, 40], 264, 1800),
+    "dgrad 64x128": ("dgrad", [130, 64, 1, 40], 264, 2440),
     "dgrad 64x64": ("dgrad", [3, 0, 5, 1], 264, 1032),
     "dgrad 64x64 split": ("dgrad", [3, 0, 70], 2312, 264),
     "wgrad 256x128": ("wgrad", [140, 0, 1, 33, 257, 64, 128, 129], 1000, 1032),
