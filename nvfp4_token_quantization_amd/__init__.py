@@ -563,13 +563,14 @@ def _out_dtype(dtype):
 
 
 def _no_overlap(out, name, *inputs):
-    """An output that shares memory with an input would be read while it is written."""
+    """An output that shares memory with an input would be read while it is
+    written, one that shares it with another output written twice."""
     if out is None or out.numel() == 0:
         return
     lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
     for t in inputs:
         if t is not None and t.numel() and t.data_ptr() < hi and lo < t.data_ptr() + t.numel() * t.element_size():
-            raise ValueError("%s must not overlap an input" % name)
+            raise ValueError("%s must not overlap an input or another output" % name)
 
 
 def _experts(offsets, groups, dev):
@@ -753,7 +754,8 @@ def nvfp4_residual_norm(x, residual=None, norm_weight=None, post_weight=None, ga
             continue
         res[key] = _out(t, "out " + key, shape, dt, dev)
         same = key == "residual" and residual is not None and t.data_ptr() == residual.data_ptr()
-        _no_overlap(t, "out " + key, x, None if same else residual, post_weight, gate, norm_weight)
+        _no_overlap(t, "out " + key, x, None if same else residual, post_weight, gate, norm_weight,
+                    *[o for k, o in res.items() if k != key])
     g = res.get
     with _on(dev):
         st = lib().nvfp4_residual_norm(_ptr(x), _type(x), _ptr(residual), _TYPES[rdt], _ptr(post_weight), _ptr(gate),
@@ -807,7 +809,8 @@ def nvfp4_residual_norm_backward(x, residual, norm_weight=None, dh=None, d_resid
             continue
         res[key] = _out(t, "out " + key, shape, dt, dev)
         same = key == "d_residual" and d_residual is not None and t.data_ptr() == d_residual.data_ptr()
-        _no_overlap(t, "out " + key, x, residual, dh, None if same else d_residual, post_weight, gate, norm_weight)
+        _no_overlap(t, "out " + key, x, residual, dh, None if same else d_residual, post_weight, gate, norm_weight,
+                    *[o for k, o in res.items() if k != key])
     g = res.get
     if workspace is None:
         with _on(dev):
@@ -816,6 +819,7 @@ def nvfp4_residual_norm_backward(x, residual, norm_weight=None, dh=None, d_resid
     else:
         _dev(workspace, "workspace", (torch.uint8,), 1)
         _same_device(dev, ("workspace", workspace))
+        _no_overlap(workspace, "workspace", x, residual, dh, d_residual, post_weight, gate, norm_weight, *res.values())
     with _on(dev):
         st = lib().nvfp4_residual_norm_backward(
             _ptr(x), _type(x), _ptr(residual), _type(residual), _ptr(post_weight), _ptr(gate), int(gate_rows),
@@ -885,7 +889,7 @@ def nvfp4_moe_combine_backward(dout, y, slot_of, weights=None, dy_dtype=torch.bf
             dw = torch.empty((tokens, topk), dtype=torch.float32, device=dev)
         else:
             _out(dw, "out d_weights", (tokens, topk), torch.float32, dev)
-            _no_overlap(dw, "out d_weights", dout, y, slot_of, weights)
+            _no_overlap(dw, "out d_weights", dout, y, slot_of, weights, dy)
         res["d_weights"] = dw
     with _on(dev):
         st = lib().nvfp4_moe_combine_backward(_ptr(dout), _type(dout), _ptr(y), _type(y), y.shape[0], _ptr(slot_of),
@@ -948,6 +952,7 @@ def nvfp4_clip_grad_norm(grads, max_norm, out=None, norm_only=False, workspace=N
     else:
         _dev(workspace, "workspace", (torch.uint8,), 1)
         _same_device(dev, ("workspace", workspace))
+        _no_overlap(workspace, "workspace", *grads, *(out or ()))
     with _on(dev):
         st = lib().nvfp4_clip_grad_norm(ptrs, outs, counts, types, n, float(max_norm), _ptr(norm), _ptr(workspace),
                                         workspace.numel(), _stream(dev))

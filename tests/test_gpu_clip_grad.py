@@ -138,3 +138,11 @@ def test_refusals():
     # the same tensors out as in, given by the caller, are in place
     kept = [t.clone() for t in g]
     check(kept, 1.0, g, nv.nvfp4_clip_grad_norm(g, 1.0, out=list(g)))
+
+
+def test_refuses_a_workspace_in_a_gradient():
+    g = [torch.ones(1 << 16, device=DEV), torch.ones(8, device=DEV)]
+    out = [torch.empty_like(t) for t in g]
+    for space in (g[0], out[0]):
+        with pytest.raises(ValueError):
+            nv.nvfp4_clip_grad_norm(g, 1.0, out=out, workspace=space.view(torch.uint8))

@@ -166,3 +166,11 @@ def test_refusals():
             bad()
     with pytest.raises(nv.NVFP4Error):
         f(c["y"], torch.zeros(1, 65, dtype=torch.int32, device=DEV))
+
+
+def test_refuses_outputs_in_one_memory():
+    c = make(6, 2, 16)
+    dy = torch.empty(c["y"].shape, dtype=torch.float32, device=DEV)
+    dw = dy.view(-1)[:12].view(6, 2)
+    with pytest.raises(ValueError):
+        nv.nvfp4_moe_combine_backward(c["dout"], c["y"], c["slot"], c["p"], out={"dy": dy, "d_weights": dw})

@@ -296,3 +296,26 @@ def test_refusals():
         nv.nvfp4_residual_norm(c["x"], c["residual"], c["norm_weight"], eps=-1.0)
     with pytest.raises(nv.NVFP4Error):
         backward(c, c["residual"], workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
+def test_refuses_outputs_and_workspaces_in_one_memory():
+    c = make(4, 264)
+    buf = torch.empty(4, 264, dtype=BF16, device=DEV)
+    one = dict(c, residual=c["residual"].to(BF16))
+    with pytest.raises(ValueError):
+        forward(one, out={"residual": buf, "h": buf})
+    stored = forward(one)["residual"]
+    one["dr"] = one["dr"].to(BF16)
+    with pytest.raises(ValueError):
+        backward(one, stored, out={"dx": buf, "d_residual": buf})
+    with pytest.raises(ValueError):
+        backward(one, stored, out={"d_residual": one["dh"]})
+    space = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    dx = space[:4 * 264 * 2].view(BF16).view(4, 264)
+    with pytest.raises(ValueError):
+        backward(one, stored, out={"dx": dx}, workspace=space)
+    # in place where the calls allow it
+    kept = one["dr"].clone()
+    want = backward(dict(one, dr=kept), stored)
+    got = backward(one, stored, out={"d_residual": one["dr"]})
+    assert torch.equal(got["d_residual"], want["d_residual"]) and torch.equal(got["dx"], want["dx"])

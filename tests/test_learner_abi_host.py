@@ -187,3 +187,13 @@ def test_binding_refuses_cpu_tensors_and_overlaps():
                         ([0, 64], [64, 128])):
         with pytest.raises(ValueError):
             nv._disjoint(grads, grads if outs is None else outs, [32, 32])
+
+
+def test_binding_finds_outputs_in_one_memory():
+    import nvfp4_token_quantization_amd as nv
+    buf = torch.zeros(64)
+    nv._no_overlap(buf[:32], "out", buf[32:], None, buf[:0])
+    nv._no_overlap(buf[:0], "out", buf)
+    for other in (buf, buf[31:], buf[:1], buf.view(torch.uint8)[127:128]):
+        with pytest.raises(ValueError):
+            nv._no_overlap(buf[:32], "out", other)
