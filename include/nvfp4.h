@@ -467,9 +467,11 @@ int nvfp4_bf16_grouped_wgrad(const uint16_t* dy, int64_t m_total, const uint16_t
  *             Any of them needs norm_weight.
  * The norm before the next block sees the rounded r', so its backward pass
  * from the stored r' is exact.  Sums of squares are held in fp32: values
- * whose row of squares overflows fp32 normalize to zero.  eps >= 0; a row of
- * zeros with eps == 0 is NaN, as the formula is.  Each row depends only on
- * its own row.  d <= 16384; q, sb, s need d % 16 == 0.
+ * whose row of squares overflows fp32 normalize to zero, and where eps does
+ * not outweigh them, squares below fp32's normal range (values under about
+ * 1e-19) lose digits of their norm.  eps >= 0; a row of zeros with eps == 0 is
+ * NaN, as the formula is.  Each row depends only on its own row.  d <= 16384;
+ * q, sb, s need d % 16 == 0.
  *
  * Backward, from dh (NULL: no gradient through h) and d_residual_out (NULL:
  * zeros), at least one of them, with x and the stored residual_out r':
@@ -478,9 +480,12 @@ int nvfp4_bf16_grouped_wgrad(const uint16_t* dy, int64_t m_total, const uint16_t
  *   f32, or (gate_rows) [rows, d] of param_type.  Any of d_residual,
  *   d_post_weight, d_gate, d_norm_weight may be NULL.
  *   d_residual_out and d_residual have residual_type and may be one buffer.
+ *   Its row sums (of b^2, r'^2 and the products of b, r' and the gradients
+ *   with the parameters) are held in fp32 and have to fit it.
  *   Column sums are added in a fixed order (no atomics).  workspace: at least
  *   nvfp4_residual_norm_backward_workspace(rows, d) bytes (it depends on the
- *   current device's number of CUs) of the caller's, 16-byte aligned, free for other use when the call's work has completed;
+ *   current device's number of CUs) of the caller's, 16-byte aligned, free for
+ *   other use when the call's work has completed;
  *   needed when one of the [d] gradients is asked for.  rows == 0 gives zero
  *   column sums.
  * Errors: INVALID_VALUE (sizes, types, eps, a missing or too small workspace,

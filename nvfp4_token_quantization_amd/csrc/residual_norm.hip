@@ -321,9 +321,11 @@ __global__ __launch_bounds__(MAXT, PLAIN || MAXT > 512 ? 4 : 3) void norm_backwa
     block_sum<6>(ss, W, slot, sums);
     const float rho1 = post ? rho_of(ss[0], p.inv_d, p.eps) : 1.0f;
     const float rho2 = norm ? rho_of(ss[1], p.inv_d, p.eps) : 0.0f;
-    const float c2 = rho2 * rho2 * rho2 * (ss[2] * p.inv_d);
+    // one rho at a time: a bare rho^3 leaves fp32 for rows of about 1e13 and
+    // 1e-13, long before their squares do
+    const float c2 = rho2 * (rho2 * (rho2 * (ss[2] * p.inv_d)));
     const float s1 = __builtin_fmaf(-c2, ss[5], __builtin_fmaf(rho2, ss[4], ss[3]));
-    const float c1 = post ? rho1 * rho1 * (s1 * p.inv_d) : 0.0f;
+    const float c1 = post ? rho1 * (rho1 * (s1 * p.inv_d)) : 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float o[8], dg[8], w2[8], q[8];

@@ -319,3 +319,55 @@ def test_refuses_outputs_and_workspaces_in_one_memory():
     want = backward(dict(one, dr=kept), stored)
     got = backward(one, stored, out={"d_residual": one["dr"]})
     assert torch.equal(got["d_residual"], want["d_residual"]) and torch.equal(got["dx"], want["dx"])
+
+
+def sized(rows, d, size, gate, r):
+    """Rows of x and of the stored residual of about `size`, a dh with a part
+    along the residual's rows, so that the projection term is as large as the
+    others, and a dr of the gradient's own size."""
+    c = make(rows, d, F32, r, F32, True, gate, seed=d)
+    c["x"] = c["x"] / 3 * size
+    stored = (c["residual"].float() / 2 * size).to(r)
+    c["dh"] = (stored.float() / size + c["dh"].float()).to(BF16)
+    c["dr"] = (c["dr"].float() / size).to(r)
+    return c, stored
+
+
+@pytest.mark.parametrize("size,eps", [(1e12, EPS), (1e14, EPS), (1e15, EPS), (1e17, EPS), (1e-13, 0.0), (1e-16, 0.0),
+                                      (1e-15, 1e-33)])
+@pytest.mark.parametrize("d,gate,r", [(264, "channel", BF16), (264, "element", F32), (77, "channel", F32), (8200, "none", BF16)])
+def test_backward_of_very_large_and_very_small_rows(size, eps, d, gate, r):
+    """rho^3 leaves fp32 long before the row of squares does."""
+    c, stored = sized(7, d, size, gate, r)
+    for dr in (c["dr"], None):
+        got = nv.nvfp4_residual_norm_backward(c["x"], stored, c["norm_weight"], c["dh"], dr, post_weight=c["post_weight"],
+                                              gate=c["gate"], scale=0.7, eps=eps, dx_dtype=F32)
+        want = ref.norm_backward(c["x"], stored, c["norm_weight"], c["dh"], dr, c["post_weight"], c["gate"], 0.7, eps)
+        assert set(got) == set(want)
+        for key, (w, bound) in want.items():
+            ref.close(got[key], w, bound, key)
+
+
+@pytest.mark.parametrize("d", [264, 77, 8200])
+def test_backward_of_zero_and_not_finite_rows(d):
+    c = make(9, d, seed=d)
+    stored = forward(c)["residual"]
+    c["x"][1] = 0
+    stored[2] = 0
+    c["x"][3] = 0
+    stored[3] = 0
+    c["dh"][4] = 0
+    c["dr"][4] = 0
+    got = backward(c, stored)
+    check_backward(c, stored, got)
+    bad, bad_stored = dict(c, x=c["x"].clone(), dh=c["dh"].clone()), stored.clone()
+    bad["x"][0, 5] = float("nan")
+    bad["dh"][5, 7] = float("inf")
+    bad_stored[8, 9] = float("nan")
+    again = backward(bad, bad_stored)
+    keep = [1, 2, 3, 4, 6, 7]
+    for key in ("dx", "d_residual"):  # each row by itself
+        assert torch.equal(again[key][keep], got[key][keep]), key
+    assert again["dx"][0].isnan().all() and torch.equal(again["d_residual"][0], got["d_residual"][0])
+    assert again["d_residual"][8].isnan().all() and again["dx"][8].isnan().all()
+    assert again["dx"][5].isnan().any()
