@@ -556,7 +556,8 @@ int nvfp4_moe_combine_backward(const void* dout, int dout_type, const void* y, i
  *   nvfp4_clip_grad_norm_workspace(tensors) bytes of the caller's, 8-byte
  *   aligned, free for other use when the call's work has completed.
  * Squares are summed in fp64 (no overflow or underflow), in a fixed order;
- * the norm is rounded once to fp32 and the factor once.  A NaN or infinite
+ * the norm is rounded once to fp32 and the factor once to 24 bits (it may lie
+ * below fp32's range, as max_norm / norm can).  A NaN or infinite
  * gradient gives a NaN or infinite norm and the formula's gradients.
  * max_norm >= 0.  Addresses are part of a captured graph, as in every call.
  * Errors: INVALID_VALUE (null arrays, negative counts, unknown types, neither

@@ -115,7 +115,14 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(ClipList l, const doubl
   const double norm = __builtin_sqrt(block_sum_f64(acc, s));
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out) *norm_out = (float)norm;
   const double f = (double)max_norm / (norm + 1e-6);
-  const float c = (float)(f > 1.0 ? 1.0 : f);  // a NaN norm gives a NaN factor
+  // The factor is rounded once to 24 bits, c 2^e: e = 0 where it is a normal
+  // fp32, else c lies in [0.5, 1] (as a subnormal fp32 it left gradients of
+  // norm 3e38 clipped to 0.001 off by 1e-4, and as zero those clipped to 1e-9
+  // zero).  A NaN norm gives a NaN factor.
+  int e = 0;
+  const bool small = f > 0.0 && f < 0x1p-126;
+  const float c = (float)(f > 1.0 ? 1.0 : small ? __builtin_frexp(f, &e) : f);
+  auto scaled = [&](float v) { return __builtin_ldexpf(v * c, e); };
   for (int chunk = l.first[l.n] - 1 - (int)blockIdx.x; chunk >= 0; chunk -= gridDim.x) {
     int t;
     int64_t lo, hi;
@@ -130,22 +137,22 @@ __global__ __launch_bounds__(256) void clip_scale_kernel(ClipList l, const doubl
         float v[8];
         load8<true>(in + lo * (bf ? 2 : 4), bf, CLIP_CHUNK, i, 256, threadIdx.x, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= c;
+        for (int k = 0; k < 8; ++k) v[k] = scaled(v[k]);
         store8<true>(out + lo * (bf ? 2 : 4), bf, CLIP_CHUNK, i, 256, threadIdx.x, v);
       }
       continue;
     }
     walk_chunk(lo, hi, wide,
-               [&](int64_t e) {
+               [&](int64_t k) {
                  float v[8];
-                 load8<true>(in + e * (bf ? 2 : 4), bf, 8, 0, 256, 0, v);
+                 load8<true>(in + k * (bf ? 2 : 4), bf, 8, 0, 256, 0, v);
 #pragma unroll
-                 for (int i = 0; i < 8; ++i) v[i] *= c;
-                 store8<true>(out + e * (bf ? 2 : 4), bf, 8, 0, 256, 0, v);
+                 for (int i = 0; i < 8; ++i) v[i] = scaled(v[i]);
+                 store8<true>(out + k * (bf ? 2 : 4), bf, 8, 0, 256, 0, v);
                },
-               [&](int64_t e) {
-                 if (bf) reinterpret_cast<uint16_t*>(out)[e] = to_bf16(bf16_to_f32(reinterpret_cast<const uint16_t*>(in)[e]) * c);
-                 else reinterpret_cast<float*>(out)[e] = reinterpret_cast<const float*>(in)[e] * c;
+               [&](int64_t k) {
+                 if (bf) reinterpret_cast<uint16_t*>(out)[k] = to_bf16(scaled(bf16_to_f32(reinterpret_cast<const uint16_t*>(in)[k])));
+                 else reinterpret_cast<float*>(out)[k] = scaled(reinterpret_cast<const float*>(in)[k]);
                });
   }
 }

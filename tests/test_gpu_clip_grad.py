@@ -146,3 +146,19 @@ def test_refuses_a_workspace_in_a_gradient():
     for space in (g[0], out[0]):
         with pytest.raises(ValueError):
             nv.nvfp4_clip_grad_norm(g, 1.0, out=out, workspace=space.view(torch.uint8))
+
+
+@pytest.mark.parametrize("std,max_norm", [(1e37, 1e-3), (1e37, 0.5), (1e20, 1e-30), (1e38, 1e-33), (1e3, 1e-34)])
+def test_factors_below_fp32(std, max_norm):
+    """max_norm / norm under fp32's normal range (down to 1e-73 here), results
+    inside it: max_norm, the factor and the product are rounded once each."""
+    for sizes in ([1000, 77], [9000, 16384]):
+        grads = tensors(sizes, std=std)
+        for t in grads:
+            t.clamp_(-3e38, 3e38)  # a draw past the type's range would be infinite
+        out = [torch.empty_like(t) for t in grads]
+        norm, (want, c) = nv.nvfp4_clip_grad_norm(grads, max_norm, out=out), exact(grads, max_norm)
+        assert float(norm) == math.inf if want > 3.5e38 else abs(float(norm) - want) <= 2 * ref.U * want
+        for i, (g, o) in enumerate(zip(grads, out)):
+            w = g.double() * c
+            ref.close(o, w, 4 * ref.U * w.abs(), "tensor %d" % i)
