@@ -13,6 +13,7 @@ same chain in 64 bits with autograd, on the chain's own rounded activations.
 import pytest
 import torch
 
+import learner_refs as ref
 import nvfp4_token_quantization_amd as nv
 
 pytestmark = pytest.mark.gpu
@@ -194,3 +195,14 @@ def test_gradients_of_microbatches_add_up_in_place():
         nv.nvfp4_bf16_grouped_wgrad(a["d_gu"], a["h_deq"], a["rt"]["offsets"], row_index=a["rt"]["row_index"], add=acc, out=acc)
     # x + x is exact; the sums inside each call have the same bits
     assert torch.equal(acc, a["d_up"] * 2)
+
+
+def test_clipped_gradients_of_the_block_element_by_element():
+    a = block(inputs(2))
+    grads = [a[k] for k in GRADS]
+    total = float(torch.stack([g.double().square().sum() for g in grads]).sum().sqrt())
+    kept = [g.clone() for g in grads]
+    nv.nvfp4_clip_grad_norm(grads, 0.25)
+    for name, g, k in zip(GRADS, grads, kept):
+        want = k.double() * (0.25 / (total + 1e-6))
+        ref.close(g, want, 4 * ref.U * want.abs(), name)
