@@ -326,3 +326,31 @@ def test_every_tile_shape_in_place_rows(shape):
     way, counts, n, k = SHAPES[shape]
     c = case(counts, n, k, seed=k)
     ref.close(run(way, c), *want(way, c), shape)
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("n,k", [(136, 264), (1032, 2312)])
+def test_rows_depend_on_their_own_rows_alone(way, n, k):
+    """Other values (and no numbers at all) in the other rows, at the same
+    sizes and offsets, leave a row's bits (an expert's, for wgrad) alone."""
+    c = case([300, 40, 0, 513], n, k, seed=16)
+    first = run(way, c)
+    for value in (2.5, float("nan"), float("inf")):
+        o = dict(c, x=c["x"].clone(), dy=c["dy"].clone())
+        if way == "wgrad":
+            for t in (o["x"], o["dy"]):
+                t[:300], t[340:] = value, value
+            assert torch.equal(run(way, o)[1], first[1])
+            continue
+        other = torch.arange(853, device=DEV) % 3 != 0
+        o["x"][other], o["dy"][other] = value, value
+        got = run(way, o)
+        assert torch.equal(got[~other], first[~other])
+        assert not torch.equal(got[other], first[other])
+
+
+def test_wgrad_output_has_the_groups_exactly():
+    c = case([17, 3], 72, 136, seed=10)
+    for groups in (1, 3):
+        with pytest.raises(ValueError):
+            run("wgrad", c, out=torch.empty(groups, 72, 136, device=DEV))
