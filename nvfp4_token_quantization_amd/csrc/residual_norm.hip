@@ -489,12 +489,15 @@ extern "C" int nvfp4_residual_norm(const void* x, int x_type, const void* residu
 #if NVFP4_CHECKED
   if (s || amax) {
     nvfp4check::Checks chk((hipStream_t)stream);
-    if (x_type == NVFP4_TYPE_BF16) chk.bf16_finite((const uint16_t*)x, rows * d);
-    else chk.f32_finite((const float*)x, rows * d);
-    if (residual) {
-      if (residual_type == NVFP4_TYPE_BF16) chk.bf16_finite((const uint16_t*)residual, rows * d);
-      else chk.f32_finite((const float*)residual, rows * d);
-    }
+    auto finite = [&](const void* t, int type, int64_t n) {
+      if (type == NVFP4_TYPE_BF16) chk.bf16_finite((const uint16_t*)t, n);
+      else chk.f32_finite((const float*)t, n);
+    };  // NULL: nothing to check
+    finite(x, x_type, rows * d);
+    finite(residual, residual_type, rows * d);
+    finite(post_weight, param_type, d);
+    finite(gate, param_type, gate_rows ? rows * d : d);
+    finite(norm_weight, param_type, d);
     if ((st = chk.result())) return st;
   }
 #endif

@@ -80,3 +80,28 @@ def test_rows_to_quantize_must_be_finite(use):
     with pytest.raises(nv.NVFP4Error) as e:
         c["norm"](out=out)
     assert e.value.status == nv.ERROR_PRECONDITION and (out["residual"] == 9).all()
+
+
+@pytest.mark.parametrize("name", ["norm_weight", "post_weight", "gate", "gate by row"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_parameters_of_rows_to_quantize_must_be_finite(use, name, dtype):
+    g = torch.Generator().manual_seed(2)
+
+    def n(*s, t=dtype):
+        return torch.randn(*s, generator=g).to(t).to(DEV)
+    x, r = n(20, 256, t=F32), n(20, 256, t=BF16)
+    p = {"norm_weight": n(256), "post_weight": n(256), "gate": n(20, 256) if name == "gate by row" else n(256)}
+    use("checked")
+    for kw in (dict(quantize=True), dict(want_amax=True)):
+        nv.nvfp4_residual_norm(x, r, **p, **kw)
+        for value in ("nan", "inf"):
+            bad = dict(p)
+            key = name.split()[0]
+            bad[key] = p[key].clone()
+            bad[key].view(-1)[-1] = float(value)
+            out = {"residual": torch.full((20, 256), 9.0, dtype=BF16, device=DEV)}
+            with pytest.raises(nv.NVFP4Error) as e:
+                nv.nvfp4_residual_norm(x, r, **bad, out=out, **kw)
+            assert e.value.status == nv.ERROR_PRECONDITION and (out["residual"] == 9).all()
+            # without anything quantized such a parameter is IEEE arithmetic's business
+            nv.nvfp4_residual_norm(x, r, **bad)
