@@ -573,6 +573,16 @@ def _no_overlap(out, name, *inputs):
             raise ValueError("%s must not overlap an input or another output" % name)
 
 
+def _given(out, *keys):
+    """The preallocated outputs of a call that takes them by name: a name it
+    does not know would be a tensor that is silently never written."""
+    out = out or {}
+    for key in out:
+        if key not in keys:
+            raise ValueError("out may hold %s (got %r)" % (", ".join(keys), key))
+    return out
+
+
 def _experts(offsets, groups, dev):
     _dev(offsets, "offsets", (torch.int32,), 1)
     if offsets.numel() != groups + 1:
@@ -720,7 +730,8 @@ def nvfp4_residual_norm(x, residual=None, norm_weight=None, post_weight=None, ga
     in the residual's dtype) and, with norm_weight, "h" (want_h), "amax"
     (want_amax: float32 [rows], max |h|) and "q", "sb", "s" (quantize: as
     nvfp4_quantize_rows(h)).  `out` may hold preallocated tensors under the
-    same keys; its "residual" may be `residual` itself.
+    same keys (those not asked for are left as they are); its "residual" may be
+    `residual` itself.
     """
     _dev(x, "x", _FLOATS, 2)
     rows, d = x.shape
@@ -745,7 +756,7 @@ def nvfp4_residual_norm(x, residual=None, norm_weight=None, post_weight=None, ga
     if quantize:
         want += [("q", (rows, d // 2), torch.uint8), ("sb", (rows, d // 16), torch.uint8),
                  ("s", (rows,), torch.float32)]
-    out = out or {}
+    out = _given(out, "residual", "h", "amax", "q", "sb", "s")
     res = {}
     for key, shape, dt in want:
         t = out.get(key)
@@ -776,8 +787,9 @@ def nvfp4_residual_norm_backward(x, residual, norm_weight=None, dh=None, d_resid
     (dx_dtype), "d_residual" (gradient of the residual that went in), and for
     the parameters given "d_post_weight", "d_norm_weight" (float32 [d]) and
     "d_gate" (float32 [d], or [rows, d] of the gate's dtype).  `out` may hold
-    preallocated tensors under these keys; its "d_residual" may be
-    `d_residual` itself.  workspace: optional uint8 tensor of at least
+    preallocated tensors under these keys (those of parameters not given are
+    left as they are); its "d_residual" may be `d_residual` itself.
+    workspace: optional uint8 tensor of at least
     nvfp4_residual_norm_backward_workspace(rows, d) bytes.
     """
     _dev(x, "x", _FLOATS, 2)
@@ -800,7 +812,7 @@ def nvfp4_residual_norm_backward(x, residual, norm_weight=None, dh=None, d_resid
         want.append(("d_gate", (rows, d), gate.dtype) if gate_rows else ("d_gate", (d,), torch.float32))
     if norm_weight is not None:
         want.append(("d_norm_weight", (d,), torch.float32))
-    out = out or {}
+    out = _given(out, "dx", "d_residual", "d_post_weight", "d_gate", "d_norm_weight")
     res = {}
     for key, shape, dt in want:
         t = out.get(key)
@@ -866,7 +878,8 @@ def nvfp4_moe_combine_backward(dout, y, slot_of, weights=None, dy_dtype=torch.bf
     """Backward pass of nvfp4_moe_combine: "dy" [rows, d] (dy[slot_of[t, j]] =
     weights[t, j] * dout[t]; rows that no slot names are not written) and,
     with weights, "d_weights" [tokens, topk].  No row may be named twice.
-    `out` may hold preallocated tensors under these keys."""
+    `out` may hold preallocated tensors under these keys ("d_weights" is left
+    as it is without weights)."""
     _dev(y, "y", _FLOATS, 2)
     dev = y.device
     tokens, topk = _slots(slot_of, weights, dev)
@@ -875,7 +888,7 @@ def nvfp4_moe_combine_backward(dout, y, slot_of, weights=None, dy_dtype=torch.bf
     if tuple(dout.shape) != (tokens, d):
         raise ValueError("dout must have shape (%d, %d) (got %s)" % (tokens, d, tuple(dout.shape)))
     _same_device(dev, ("dout", dout))
-    out = out or {}
+    out = _given(out, "dy", "d_weights")
     dy = out.get("dy")
     if dy is None:
         dy = torch.empty(tuple(y.shape), dtype=_out_dtype(dy_dtype), device=dev)

@@ -174,3 +174,13 @@ def test_refuses_outputs_in_one_memory():
     dw = dy.view(-1)[:12].view(6, 2)
     with pytest.raises(ValueError):
         nv.nvfp4_moe_combine_backward(c["dout"], c["y"], c["slot"], c["p"], out={"dy": dy, "d_weights": dw})
+
+
+def test_outputs_of_other_names():
+    c = make(6, 2, 16)
+    dw = torch.full((6, 2), 7.0, device=DEV)
+    for name in ("dw", "dx", "d_weight"):
+        with pytest.raises(ValueError):
+            nv.nvfp4_moe_combine_backward(c["dout"], c["y"], c["slot"], c["p"], out={name: dw})
+    back = nv.nvfp4_moe_combine_backward(c["dout"], c["y"], c["slot"], out={"d_weights": dw})
+    assert set(back) == {"dy"} and (dw == 7).all()

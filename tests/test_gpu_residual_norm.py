@@ -371,3 +371,23 @@ def test_backward_of_zero_and_not_finite_rows(d):
     assert again["dx"][0].isnan().all() and torch.equal(again["d_residual"][0], got["d_residual"][0])
     assert again["d_residual"][8].isnan().all() and again["dx"][8].isnan().all()
     assert again["dx"][5].isnan().any()
+
+
+def test_outputs_of_other_names():
+    """A name that the call does not know is refused before anything is
+    written; an output it knows but was not asked for stays as it is."""
+    c = make(5, 264)
+    kept = {"residual": torch.full((5, 264), 3.0, dtype=BF16, device=DEV)}
+    for name in ("residual_out", "d_residual", "H"):
+        with pytest.raises(ValueError):
+            forward(c, out=dict(kept, **{name: torch.empty(5, 264, dtype=BF16, device=DEV)}))
+    assert (kept["residual"] == 3).all()
+    amax = torch.full((5,), 7.0, device=DEV)
+    got = forward(c, out={"amax": amax})
+    assert "amax" not in got and (amax == 7).all()
+    stored = got["residual"]
+    with pytest.raises(ValueError):
+        backward(c, stored, out={"d_x": torch.empty(5, 264, dtype=BF16, device=DEV)})
+    gate = torch.full((264,), 7.0, device=DEV)
+    back = backward(dict(c, gate=None), stored, out={"d_gate": gate})
+    assert "d_gate" not in back and (gate == 7).all()
