@@ -8,9 +8,11 @@
 // bf16 products are exact in fp32 and summed there by the MFMAs; an output is
 // rounded once.  One expert of 8192 rows, n = k = 8192 (bf16 output): forward
 // 1298 TFLOP/s, dgrad 1196, wgrad 1190, where a large library product
-// reaches 1377.  Ragged layouts are bound by HBM and by padding to 64-row
-// slabs: 32768 rows over 128 Zipf experts, n = 1536, k = 2048, fp32 output: 302
-// us forward (3.3 TB/s of its bytes, 682 TFLOP/s), 446 us wgrad (3.9 TB/s).
+// reaches 1377.  Ragged layouts are bound by what they move through HBM, panels
+// read more than once among it, and by padding to 64-row slabs: 32768 rows over
+// 128 Zipf experts, n = 1536, k = 2048, fp32 output: forward 295 to 314 us (682
+// TFLOP/s at 302; reads 1.32 GB where 0.78 GB are the operands), wgrad 441 to
+// 458 us (reads 0.95 GB for 0.12 GB and writes 1.61 GB).
 #include <type_traits>
 
 #include "gemm_common.h"
@@ -52,8 +54,8 @@ struct Bf16Args {
 //     ds_read_b64_tr_b16, which hands each lane 4 summed elements of its
 //     column.  Chunks are XOR-swizzled by row so that the four rows of 16
 //     lanes (and of 32) lie in different banks.
-// Neither layout shows bank conflicts in the counters (SQ_LDS_BANK_CONFLICT 0;
-// 4% of the LDS cycles of the row reads beside column reads in dgrad).
+// Row reads show no bank conflicts in the counters; with column reads they
+// take 3% of the LDS cycles in dgrad (one column operand) and 13% in wgrad (two).
 // Rows, columns and summed elements that do not exist get an offset past the
 // resource, for which the DMA writes zeros.
 constexpr uint32_t BG_OOB = 0x80000000u;
@@ -391,9 +393,11 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
 // light ones are mixed evenly among the heavy ones, but for an eighth of all
 // tiles kept for the end, where short tiles level the finish (32768 rows over
 // 128 Zipf experts, n = 1536, k = 2048: 299 us; heavy ones first 324).  An
-// expert's heavy tiles go in bands of 4 m-tiles.  Every wave derives this from
-// the device offsets by wave scans in registers (G experts in NSEG segments
-// of 64 lanes).  False: no tile (block-uniform).
+// expert's heavy tiles go in bands of 4 m-tiles; a W past an XCD's 4 MB of L2
+// (6.3 MB here) is read again by each band and by the light remainder, a part
+// of the 0.54 GB that this layout reads beyond its operands.  Every wave
+// derives this from the device offsets by wave scans in registers (G experts
+// in NSEG segments of 64 lanes).  False: no tile (block-uniform).
 template <int NSEG, int TM, int TN>
 __device__ __forceinline__ bool bg_schedule(const int32_t* offsets, int G, int64_t m_total, int tn, int lane, TileRange& out) {
   constexpr int BM = 64 * TM;
@@ -476,7 +480,7 @@ __device__ __forceinline__ bool bg_schedule(const int32_t* offsets, int G, int64
 // writes push the panels that an expert's tiles share out of the L2s; in
 // expert order 513).  XCD x takes every eighth tile of both lists, so that an
 // expert's tiles of one block of X columns share an L2 where the columns
-// come in eighths.
+// come in eighths; every XCD then reads all of dY (eight times 100 MB there).
 template <int NSEG>
 __device__ __forceinline__ bool bg_schedule_wgrad(const int32_t* offsets, int G, int64_t m_total, int tiles, int lane,
                                                   int64_t& row_lo, int64_t& row_hi, int& g, int& tile) {
@@ -694,9 +698,10 @@ static void launch_tiles(const Bf16Args& a, hipStream_t str) {
 //    one's work where they do not (32768 rows over 8 Zipf experts, n = k =
 //    1024: 128 x 128 192 us against 244; equal experts 93 and 92).
 //  - few tiles and a long sum: two wave groups of a block halve the chain (64
-//    rows, n = k = 4096: 18.3 us against 21.5; wgrad of 15262 rows over 3
-//    experts, n = 784, k = 104: 71 against 108; four groups gain no more: a
-//    CU's loads bound them).
+//    rows, n = k = 4096: 18.3 us against 21.5, where its bytes alone take 6;
+//    wgrad of 15262 rows over 3 experts, n = 784, k = 104: 71 against 108, its
+//    bytes 5: few CUs have work; four groups gain no more: a CU's loads bound
+//    them).
 template <int MODE>
 static int launch_bf16(const Bf16Args& p, hipStream_t str) {
   const int64_t cus = nvfp4host::num_cus();

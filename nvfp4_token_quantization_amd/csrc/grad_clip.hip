@@ -21,8 +21,9 @@ namespace nvfp4 {
 constexpr int CLIP_LIST = 96;        // tensors in one launch's arguments
 constexpr int CLIP_CHUNK = 8192;     // elements a block takes at a time
 // Blocks, and partial sums, of one launch: three a CU (755 MB of fp32 and bf16
-// gradients, 512, 768, 1024, 2048 blocks: 452, 410, 419, 450 us; 5.5 TB/s over
-// the three passes at 768, the norm alone 133 us, 5.7 TB/s).
+// gradients, 512, 768, 1024, 2048 blocks: 452, 410, 419, 450 us; as it stands
+// 397 to 405 us into tensors of their own, 5.6 TB/s over the three passes, 408
+// with ordinary stores, 423 in place; the norm alone 129 us, 5.8 TB/s).
 constexpr int CLIP_BLOCKS = 768;
 
 struct ClipList {

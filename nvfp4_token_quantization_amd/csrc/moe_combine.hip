@@ -10,9 +10,10 @@
 // first sum, choices added in order j in fp32 (the same bits on every call).
 // Backward: one block per token; its waves walk the columns, hold the token's
 // gradient piece once for all choices, and the dot products meet in LDS in
-// wave order.  4096 tokens x 8 x 2048, fp32 y: forward 42 us (6.8 TB/s: part of y
-// is still in the memory-side cache), backward 65 us (6.4 TB/s; 85 with
-// ordinary stores of dy).
+// wave order.  4096 tokens x 8 x 2048, fp32 y, bf16 dy, inputs changing from
+// call to call: forward 52 us (5.5 TB/s), backward 82 us (5.1 TB/s; 81 with
+// ordinary stores of dy).  On the same inputs again and again part of y is
+// still in the memory-side cache: 42 and 65 us, there 85 with ordinary stores.
 #include "rowwise.h"
 
 namespace nvfp4 {

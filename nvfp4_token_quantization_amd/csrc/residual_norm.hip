@@ -15,9 +15,10 @@
 // HBM-bound: every row is read once and stays in registers (W = ceil(d / 512)
 // waves hold 8 elements a thread, 16 past d = 8192).  The parameters are the
 // same for every row, so a block keeps them in registers and walks rows; the
-// next row's loads are issued before the current row's reductions.  A row's
-// bytes meet the copy rate of the card (16384 x 2560, fp32 block output, bf16
-// residual: forward 76 us, 5.5 TB/s; backward 118 us, 5.0 TB/s).  The
+// next row's loads are issued before the current row's reductions.  Rows of
+// 512 to 8192 come near the card's copy rate of 6.1 TB/s (16384 x 2560, fp32
+// block output, bf16 residual, post norm, channel gate: forward 73 to 76 us, 5.6
+// TB/s, 82 with the NVFP4 rows too; backward 114 to 117 us, 5.1 TB/s).  The
 // backward pass keeps its column sums in registers too, and writes one
 // partial row per block, which a second kernel adds in block order (no
 // atomics: the same bits on every call).
@@ -208,7 +209,10 @@ __global__ __launch_bounds__(MAXT) void norm_forward_kernel(NormArgs p) {
 // have to hide: with two exchanges, divisions and branches for every optional
 // part a row took about 3 us and 16384 x 2560 rows 250 us.  PLAIN: post and
 // next norm, both gradients, no gate by rows, known when compiled, and at
-// most 128 registers (four waves a SIMD).
+// most 128 registers (four waves a SIMD).  The other forms are slower (16384 x
+// 2560 without post norm and gate 193 us against 117), and 1024 threads leave
+// them 128 registers too: they spill 1 to 27 of them for 4096 < d <= 8192 and
+// 96 to 135 beyond, where PLAIN spills 3 to 10.
 template <int NV, int KIND, int MAXT, bool PLAIN>
 __global__ __launch_bounds__(MAXT, PLAIN || MAXT > 512 ? 4 : 3) void norm_backward_kernel(NormArgs p) {
   typedef Rows<KIND> R;
