@@ -570,6 +570,134 @@ int nvfp4_clip_grad_norm(const void* const* grads, void* const* out, const int64
                          const int32_t* types, int64_t tensors, float max_norm, float* norm,
                          void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * The router's gate: the weights of a token's chosen experts, the load of the
+ * experts and the balance loss, and their gradient.
+ *
+ *   p[t] = softmax(logits[t])
+ *   weights[t, j] = p[t, e_j]            e_j = experts[t, j]
+ *                   (normalize: p[t, e_j] / sum over j' of p[t, e_j'])
+ *   counts[e] = choices of expert e;  counts[num_experts] = N, tokens counted
+ *   prob_sums[e] = sum over t of p[t, e]
+ *   loss = num_experts * sum_e (counts[e] / sum of counts) (prob_sums[e] / N)
+ *
+ * weights are those of nvfp4_moe_combine, experts what nvfp4_moe_route chose.
+ * The pages describe no gate: the formulas above are the definition.  An even
+ * load and even probabilities give loss 1; without a counted token it is 0.
+ *
+ *   logits   [tokens, num_experts] f32;  experts [tokens, topk] i32: an index
+ *            outside [0, num_experts) is no choice (weight 0, not counted).
+ *   valid    NULL or [tokens] u8: a token whose byte is 0 is padding: its
+ *            weights are 0, it is not counted, and whatever its logits hold
+ *            goes into nothing.
+ *   weights  [tokens, topk] f32;  counts [num_experts + 1] i32, prob_sums
+ *            [num_experts] f32, loss [1] f32: all three or none.
+ *   workspace: nvfp4_moe_gate_workspace(tokens, num_experts) bytes of the
+ *            caller's (0 for few tokens), 4-byte aligned, needed for those
+ *            three, free for other use when the call's work has completed.
+ * Backward: d_logits from d_weights (NULL: no gradient through the weights)
+ * and d_loss ([1] f32 device, with the loss's coefficient; NULL: none), at
+ * least one.  counts are constants of the loss, as forward gave them or summed
+ * over several ranks: prob_sums then count against the summed N, and the
+ * ranks' losses add up.  Padding tokens get zeros.
+ * Softmax and sums in fp32, the loss from its sums in fp64.  An expert whose
+ * logit is -infinity has p = 0; NaN or +infinity make their own token's
+ * values NaN (and with them prob_sums and loss).  Deterministic (integer
+ * counts; float sums in a fixed order).  num_experts <= 1024, topk <= 64 and
+ * <= num_experts, tokens * topk < 2^31.
+ * Errors: INVALID_VALUE (sizes, null pointers with work, one or two of the
+ * three, a missing or too small workspace, neither d_weights nor d_loss,
+ * d_loss without counts), UNSUPPORTED_SHAPE, MISALIGNED (4 bytes), ARCH,
+ * LAUNCH.
+ */
+int64_t nvfp4_moe_gate_workspace(int64_t tokens, int64_t num_experts);
+int nvfp4_moe_gate(const float* logits, const int32_t* experts, const uint8_t* valid, int64_t tokens,
+                   int64_t num_experts, int64_t topk, int normalize, float* weights, int32_t* counts,
+                   float* prob_sums, float* loss, void* workspace, int64_t workspace_bytes,
+                   void* stream);
+int nvfp4_moe_gate_backward(const float* logits, const int32_t* experts, const uint8_t* valid,
+                            const int32_t* counts, int64_t tokens, int64_t num_experts, int64_t topk,
+                            int normalize, const float* d_weights, const float* d_loss,
+                            float* d_logits, void* stream);
+
+/*
+ * Embedding lookup with a scale, and the table's gradient by sorted tokens.
+ *
+ *   out[i] = scale * table[ids[i]]
+ *   dtable[v] = add[v] + scale * sum over tokens i with ids[i] = v of dout[i]
+ *
+ * The tokens' way into the layers; the pages describe none: the formulas above
+ * are the definition.
+ *
+ *   table [vocab, d], out and dout [tokens, d], dtable [vocab, d]: fp32 or
+ *   bf16 each.  ids [tokens] i32: an id outside [0, vocab) gives a row of
+ *   zeros and no gradient.
+ *   add NULL (zeros) or [vocab, d] of dtable's type; may be dtable itself:
+ *   then only the rows that a token names are read and written.
+ *   workspace: nvfp4_embedding_backward_workspace(tokens, d) bytes of the
+ *   caller's, 16-byte aligned, free for other use when the call's work has
+ *   completed.
+ * Sums in fp32, of a row's tokens in an order that depends on ids alone (no
+ * atomics); an output is rounded once.  tokens <= 2^24, d <= 2^20, vocab <
+ * 2^31 - 1.
+ * Errors: INVALID_VALUE (sizes, types, null pointers with work, a missing or
+ * too small workspace), UNSUPPORTED_SHAPE, MISALIGNED (elements to their size,
+ * workspace 16 bytes), ARCH, LAUNCH.
+ */
+int nvfp4_embedding(const void* table, int table_type, int64_t vocab, const int32_t* ids,
+                    int64_t tokens, int64_t d, float scale, void* out, int out_type, void* stream);
+int64_t nvfp4_embedding_backward_workspace(int64_t tokens, int64_t d);
+int nvfp4_embedding_backward(const void* dout, int dout_type, const int32_t* ids, int64_t tokens,
+                             int64_t vocab, int64_t d, float scale, const void* add, void* dtable,
+                             int dtable_type, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Negative log-probability of each row's target over a vocabulary, without
+ * the logits, and its gradients.
+ *
+ *   z[r, v] = scale <h[r], w[v]>     (scale: one over the temperature)
+ *   lse[r] = log sum_v exp(z[r, v]);  loss[r] = lse[r] - z[r, targets[r]]
+ *   dz[r, v] = scale d_loss[r] (exp(z[r, v] - lse[r]) - [v = targets[r]])
+ *   dh = dz w;  dw = add + dz^T h
+ *
+ * -loss is the log-probability that learner and sampler compare (the TRIAGE
+ * page, section 前置知识); a policy gradient is d_loss.
+ *
+ *   h [rows, k] bf16;  w [vocab, k] bf16;  targets [rows] i32: a row whose
+ *   target is outside [0, vocab) has none: its loss and lse are 0, its dh is
+ *   0, and neither its h nor its d_loss reaches any result.  Such rows cost
+ *   nothing: the products run over the others alone.
+ *   loss, lse, d_loss [rows] f32;  lse of the backward pass: what forward gave.
+ *   dh NULL or [rows, k] bf16;  dw NULL or [vocab, k] of dw_type, not both
+ *   NULL;  add NULL (zeros) or [vocab, k] of dw's type, may be dw itself.
+ *   workspace: nvfp4_vocab_loss_workspace(rows, vocab, k) or
+ *   nvfp4_vocab_loss_backward_workspace(rows, vocab, k) bytes of the caller's,
+ *   16-byte aligned, free for other use when the call's work has completed.
+ *   The backward pass goes through the vocabulary in pieces; the workspace
+ *   holds dz of one of them.
+ * Products of bf16 are exact and summed in fp32, softmax and sums are fp32.
+ * dz is rounded once to bf16 for the two products that read it (at most 2^-8
+ * of each term), dh and a bf16 dw once more.  A row with a NaN or +infinite
+ * logit has a NaN loss; a logit of -infinity has probability 0.  Probabilities
+ * and dz below fp32's normal range (2^-126) may be taken as zero.
+ * Deterministic: no atomics, and a row's results do not depend on which rows
+ * have targets other than through the order of the sums of dw.
+ * k % 8 == 0, k <= 2^20, vocab <= 2^24, rows * k < 2^30; scale finite.
+ * Errors: INVALID_VALUE (sizes, types, a scale that is not finite, null
+ * pointers with work, a missing or too small workspace), UNSUPPORTED_SHAPE,
+ * MISALIGNED (h, w, add, dh, dw and workspace 16 bytes, the rest 4), ARCH,
+ * LAUNCH.
+ */
+int64_t nvfp4_vocab_loss_workspace(int64_t rows, int64_t vocab, int64_t k);
+int nvfp4_vocab_loss(const uint16_t* h, const uint16_t* w, const int32_t* targets, int64_t rows,
+                     int64_t vocab, int64_t k, float scale, float* loss, float* lse, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+int64_t nvfp4_vocab_loss_backward_workspace(int64_t rows, int64_t vocab, int64_t k);
+int nvfp4_vocab_loss_backward(const uint16_t* h, const uint16_t* w, const int32_t* targets,
+                              const float* lse, const float* d_loss, int64_t rows, int64_t vocab,
+                              int64_t k, float scale, const void* add, uint16_t* dh, void* dw,
+                              int dw_type, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,12 @@ Functions keep the C names:
   nvfp4_moe_combine(y, slot_of, weights=None)                     -> out
   nvfp4_moe_combine_backward(dout, y, slot_of, weights=None)      -> {"dy", "d_weights"}
   nvfp4_clip_grad_norm(grads, max_norm, out=None)                 -> norm
+  nvfp4_moe_gate(logits, experts, valid=None, normalize=True)     -> {"weights", "counts", ...}
+  nvfp4_moe_gate_backward(logits, experts, counts, d_weights=None, d_loss=None) -> d_logits
+  nvfp4_embedding(table, ids, scale=1.0)                          -> out
+  nvfp4_embedding_backward(dout, ids, vocab, scale=1.0, add=None) -> dtable
+  nvfp4_vocab_loss(h, w, targets, scale=1.0)                      -> {"loss", "lse"}
+  nvfp4_vocab_loss_backward(h, w, targets, lse, d_loss, scale=1.0, add=None) -> {"dh", "dw"}
 
 (The codec self-test hooks live in the test-only ``selftest`` submodule over
 ``libnvfp4_selftest.so``.)
@@ -99,9 +105,20 @@ def load(path):
     L.nvfp4_residual_norm_backward_workspace.restype = I64
     L.nvfp4_clip_grad_norm_workspace.argtypes = [I64]
     L.nvfp4_clip_grad_norm_workspace.restype = I64
+    L.nvfp4_moe_gate.argtypes = [P, P, P, I64, I64, I64, I32, P, P, P, P, P, I64, P]
+    L.nvfp4_moe_gate_backward.argtypes = [P, P, P, P, I64, I64, I64, I32, P, P, P, P]
+    L.nvfp4_embedding.argtypes = [P, I32, I64, P, I64, I64, F32, P, I32, P]
+    L.nvfp4_embedding_backward.argtypes = [P, I32, P, I64, I64, I64, F32, P, P, I32, P, I64, P]
+    L.nvfp4_vocab_loss.argtypes = [P, P, P, I64, I64, I64, F32, P, P, P, I64, P]
+    L.nvfp4_vocab_loss_backward.argtypes = [P, P, P, P, P, I64, I64, I64, F32, P, P, P, I32, P, I64, P]
+    for f, n in (("nvfp4_moe_gate_workspace", 2), ("nvfp4_embedding_backward_workspace", 2),
+                 ("nvfp4_vocab_loss_workspace", 3), ("nvfp4_vocab_loss_backward_workspace", 3)):
+        getattr(L, f).argtypes = [I64] * n
+        getattr(L, f).restype = I64
     for f in ("nvfp4_bf16_grouped_gemm", "nvfp4_bf16_grouped_dgrad", "nvfp4_bf16_grouped_wgrad",
               "nvfp4_residual_norm", "nvfp4_residual_norm_backward", "nvfp4_moe_combine",
-              "nvfp4_moe_combine_backward", "nvfp4_clip_grad_norm"):
+              "nvfp4_moe_combine_backward", "nvfp4_clip_grad_norm", "nvfp4_moe_gate", "nvfp4_moe_gate_backward",
+              "nvfp4_embedding", "nvfp4_embedding_backward", "nvfp4_vocab_loss", "nvfp4_vocab_loss_backward"):
         getattr(L, f).restype = ctypes.c_int
     for f in ("nvfp4_quantize_rows", "nvfp4_quantize_weight", "nvfp4_gemm",
               "nvfp4_swiglu_quantize_rows", "nvfp4_moe_route", "nvfp4_dequantize_rows",
@@ -990,3 +1007,278 @@ def _disjoint(grads, outs, sizes):
         k = bisect.bisect_left(starts, lo + size) - 1  # the last output that starts below the gradient's end
         if size and k >= 0 and spans[k][1] > lo and (spans[k][0] != lo or spans[k][2] != i):
             raise ValueError("out must not overlap another gradient (tensor %d)" % i)
+
+
+def _workspace(t, need, dev, *others):
+    """The caller's workspace, checked, or one of `need` bytes for this call."""
+    if t is None:
+        return torch.empty((need,), dtype=torch.uint8, device=dev)
+    _dev(t, "workspace", (torch.uint8,), 1)
+    _same_device(dev, ("workspace", t))
+    _no_overlap(t, "workspace", *others)
+    return t
+
+
+def _gate_inputs(logits, experts, valid):
+    _dev(logits, "logits", (torch.float32,), 2)
+    _dev(experts, "experts", (torch.int32,), 2)
+    T, E = logits.shape
+    if experts.shape[0] != T:
+        raise ValueError("experts must have one row per token (got %s for %d tokens)" % (tuple(experts.shape), T))
+    if valid is not None:
+        _dev(valid, "valid", (torch.bool, torch.uint8), 1)
+        if valid.numel() != T:
+            raise ValueError("valid must have one entry per token")
+    _same_device(logits.device, ("experts", experts), ("valid", valid))
+    return T, E, experts.shape[1], logits.device
+
+
+def nvfp4_moe_gate(logits, experts, valid=None, normalize=True, balance=True, out=None, workspace=None):
+    """The router's gate: the weights of each token's chosen experts, and with
+    `balance` the experts' load and the balance loss.
+
+    logits float32 [tokens, experts]; experts int32 [tokens, topk], as
+    nvfp4_moe_route chose them (an index that is no expert is no choice);
+    valid optional bool or uint8 [tokens], false for padding.  Returns a dict:
+    "weights" float32 [tokens, topk], softmax(logits) at the chosen experts,
+    divided by their sum with `normalize`; "counts" int32 [experts + 1],
+    choices of each expert and, last, the tokens counted; "prob_sums" float32
+    [experts], sums of softmax(logits); "loss", float32 scalar, experts *
+    sum_e counts_e / sum(counts) * prob_sums_e / tokens counted.  `out` may
+    hold preallocated tensors under these keys (those not asked for are left
+    as they are); workspace: optional uint8 tensor of at least
+    nvfp4_moe_gate_workspace(tokens, experts) bytes.
+    """
+    T, E, K, dev = _gate_inputs(logits, experts, valid)
+    want = [("weights", (T, K), torch.float32)]
+    if balance:
+        want += [("counts", (E + 1,), torch.int32), ("prob_sums", (E,), torch.float32), ("loss", (), torch.float32)]
+    out = _given(out, "weights", "counts", "prob_sums", "loss")
+    res = {}
+    for key, shape, dt in want:
+        t = out.get(key)
+        if t is None:
+            res[key] = torch.empty(shape, dtype=dt, device=dev)
+            continue
+        res[key] = _out(t, "out " + key, shape, dt, dev)
+        _no_overlap(t, "out " + key, logits, experts, valid, *[o for k, o in res.items() if k != key])
+    g = res.get
+    workspace = _workspace(workspace, lib().nvfp4_moe_gate_workspace(T, E) if balance else 0, dev, logits, experts, valid,
+                           *res.values())
+    with _on(dev):
+        st = lib().nvfp4_moe_gate(_ptr(logits), _ptr(experts), _ptr(valid), T, E, K, int(bool(normalize)),
+                                  _ptr(res["weights"]), _ptr(g("counts")), _ptr(g("prob_sums")), _ptr(g("loss")),
+                                  _ptr(workspace), workspace.numel(), _stream(dev))
+    _check("nvfp4_moe_gate", st)
+    return res
+
+
+def nvfp4_moe_gate_backward(logits, experts, counts=None, d_weights=None, d_loss=None, valid=None, normalize=True,
+                            out=None):
+    """Backward pass of nvfp4_moe_gate: d_logits float32 [tokens, experts].
+
+    d_weights float32 [tokens, topk] (as nvfp4_moe_combine_backward returns
+    it) and d_loss, a float32 tensor of one element with the loss's
+    coefficient; either may be None.  counts (needed with d_loss): forward's,
+    or their sum over several ranks.  Padding tokens get zeros.
+    """
+    T, E, K, dev = _gate_inputs(logits, experts, valid)
+    if d_weights is None and d_loss is None:
+        raise ValueError("d_weights or d_loss must be given")
+    if d_weights is not None:
+        _dev(d_weights, "d_weights", (torch.float32,), 2)
+        if tuple(d_weights.shape) != (T, K):
+            raise ValueError("d_weights must have shape (%d, %d) (got %s)" % (T, K, tuple(d_weights.shape)))
+    if d_loss is not None:
+        if counts is None:
+            raise ValueError("d_loss needs counts")
+        _dev(d_loss, "d_loss", (torch.float32,))
+        if d_loss.numel() != 1:
+            raise ValueError("d_loss must have one element")
+    if counts is not None:
+        _dev(counts, "counts", (torch.int32,), 1)
+        if counts.numel() != E + 1:
+            raise ValueError("counts must have experts + 1 entries")
+    _same_device(dev, ("counts", counts), ("d_weights", d_weights), ("d_loss", d_loss))
+    if out is None:
+        out = torch.empty((T, E), dtype=torch.float32, device=dev)
+    else:
+        _out(out, "out", (T, E), torch.float32, dev)
+        _no_overlap(out, "out", logits, experts, valid, counts, d_weights, d_loss)
+    with _on(dev):
+        st = lib().nvfp4_moe_gate_backward(_ptr(logits), _ptr(experts), _ptr(valid), _ptr(counts), T, E, K,
+                                           int(bool(normalize)), _ptr(d_weights), _ptr(d_loss), _ptr(out), _stream(dev))
+    _check("nvfp4_moe_gate_backward", st)
+    return out
+
+
+def nvfp4_embedding(table, ids, scale=1.0, out=None, out_dtype=torch.bfloat16):
+    """Rows of a table by token id: out[i] = scale * table[ids[i]].  table
+    [vocab, d] float32 or bfloat16; ids int32 of any shape (an id outside the
+    table gives a row of zeros).  Returns [*ids.shape, d]."""
+    _dev(table, "table", _FLOATS, 2)
+    _dev(ids, "ids", (torch.int32,))
+    vocab, d = table.shape
+    dev = table.device
+    _same_device(dev, ("ids", ids))
+    shape = tuple(ids.shape) + (d,)
+    if out is None:
+        out = torch.empty(shape, dtype=_out_dtype(out_dtype), device=dev)
+    else:
+        _out(out, "out", shape, _out_dtype(out.dtype), dev)
+        _no_overlap(out, "out", table, ids)
+    with _on(dev):
+        st = lib().nvfp4_embedding(_ptr(table), _type(table), vocab, _ptr(ids), ids.numel(), d, float(scale), _ptr(out),
+                                   _type(out), _stream(dev))
+    _check("nvfp4_embedding", st)
+    return out
+
+
+def nvfp4_embedding_backward(dout, ids, vocab, scale=1.0, add=None, out=None, out_dtype=torch.float32, workspace=None):
+    """Backward pass of nvfp4_embedding: dtable[v] = add[v] + scale * the sum
+    of dout's rows i with ids[i] = v.
+
+    dout [*ids.shape, d] float32 or bfloat16; ids int32; add optional [vocab,
+    d] of the output's dtype, which may be `out` itself: then only the rows
+    that a token names are touched (a table shared with the loss: add and out
+    are the dw of nvfp4_vocab_loss_backward).  Returns [vocab, d].  workspace:
+    optional uint8 tensor of at least
+    nvfp4_embedding_backward_workspace(tokens, d) bytes.
+    """
+    _dev(dout, "dout", _FLOATS)
+    _dev(ids, "ids", (torch.int32,))
+    if dout.dim() < 1 or tuple(dout.shape[:-1]) != tuple(ids.shape):
+        raise ValueError("dout must have shape %s + [d] (got %s)" % (tuple(ids.shape), tuple(dout.shape)))
+    d, n, vocab = dout.shape[-1], ids.numel(), int(vocab)
+    dev = dout.device
+    _same_device(dev, ("ids", ids), ("add", add))
+    if vocab < 0:
+        raise ValueError("vocab must not be negative")
+    shape = (vocab, d)
+    if add is not None:
+        _dev(add, "add", _FLOATS, 2)
+        if tuple(add.shape) != shape:
+            raise ValueError("add must have shape %s (got %s)" % (shape, tuple(add.shape)))
+    if out is None:
+        out = torch.empty(shape, dtype=_out_dtype(out_dtype) if add is None else add.dtype, device=dev)
+    else:
+        _out(out, "out", shape, _out_dtype(out.dtype), dev)
+        _no_overlap(out, "out", dout, ids)
+    if add is not None:
+        if add.dtype != out.dtype:
+            raise TypeError("add must have the output's dtype %s (got %s)" % (out.dtype, add.dtype))
+        if add.data_ptr() != out.data_ptr():
+            _no_overlap(out, "out", add)
+    workspace = _workspace(workspace, lib().nvfp4_embedding_backward_workspace(n, d), dev, dout, ids, add, out)
+    with _on(dev):
+        st = lib().nvfp4_embedding_backward(_ptr(dout), _type(dout), _ptr(ids), n, vocab, d, float(scale), _ptr(add),
+                                            _ptr(out), _type(out), _ptr(workspace), workspace.numel(), _stream(dev))
+    _check("nvfp4_embedding_backward", st)
+    return out
+
+
+def _vocab_inputs(h, w, targets):
+    _dev(h, "h", (torch.bfloat16,), 2)
+    _dev(w, "w", (torch.bfloat16,), 2)
+    _dev(targets, "targets", (torch.int32,), 1)
+    rows, k = h.shape
+    if w.shape[1] != k:
+        raise ValueError("h and w must have the same k")
+    if targets.numel() != rows:
+        raise ValueError("targets must have one entry per row")
+    _same_device(h.device, ("w", w), ("targets", targets))
+    return rows, w.shape[0], k, h.device
+
+
+def _row_values(t, name, rows, dev):
+    _dev(t, name, (torch.float32,), 1)
+    if t.numel() != rows:
+        raise ValueError("%s must have one entry per row" % name)
+    _same_device(dev, (name, t))
+
+
+def nvfp4_vocab_loss(h, w, targets, scale=1.0, out=None, workspace=None):
+    """Negative log-probability of each row's target over the vocabulary,
+    softmax(scale * h w^T), without the logits.
+
+    h bf16 [rows, k]; w bf16 [vocab, k]; targets int32 [rows], outside [0,
+    vocab) for rows that have none (their loss and lse are 0, and they cost
+    nothing).  Returns {"loss", "lse"}, float32 [rows]; -loss is the
+    log-probability, lse what the backward pass needs.  `out` may hold
+    preallocated tensors under these keys; workspace: optional uint8 tensor of
+    at least nvfp4_vocab_loss_workspace(rows, vocab, k) bytes.  k % 8 == 0.
+    """
+    rows, vocab, k, dev = _vocab_inputs(h, w, targets)
+    out = _given(out, "loss", "lse")
+    res = {}
+    for key in ("loss", "lse"):
+        t = out.get(key)
+        if t is None:
+            res[key] = torch.empty((rows,), dtype=torch.float32, device=dev)
+            continue
+        res[key] = _out(t, "out " + key, (rows,), torch.float32, dev)
+        _no_overlap(t, "out " + key, h, w, targets, *[o for n, o in res.items() if n != key])
+    workspace = _workspace(workspace, lib().nvfp4_vocab_loss_workspace(rows, vocab, k), dev, h, w, targets, *res.values())
+    with _on(dev):
+        st = lib().nvfp4_vocab_loss(_ptr(h), _ptr(w), _ptr(targets), rows, vocab, k, float(scale), _ptr(res["loss"]),
+                                    _ptr(res["lse"]), _ptr(workspace), workspace.numel(), _stream(dev))
+    _check("nvfp4_vocab_loss", st)
+    return res
+
+
+def nvfp4_vocab_loss_backward(h, w, targets, lse, d_loss, scale=1.0, add=None, want_dh=True, want_dw=True,
+                              dw_dtype=torch.float32, out=None, workspace=None):
+    """Backward pass of nvfp4_vocab_loss.
+
+    lse: what forward gave; d_loss float32 [rows], the gradient of each row's
+    loss (not read into anything where the row has no target); add optional
+    [vocab, k] of dw's dtype, which may be out's "dw" itself (gradients of
+    several microbatches added up in place).  Returns a dict: "dh" bf16 [rows,
+    k] (zeros without a target; want_dh) and "dw" [vocab, k] of dw_dtype
+    (want_dw).  `out` may hold preallocated tensors under these keys (those not
+    asked for are left as they are); workspace: optional uint8 tensor of at
+    least nvfp4_vocab_loss_backward_workspace(rows, vocab, k) bytes.
+    """
+    rows, vocab, k, dev = _vocab_inputs(h, w, targets)
+    _row_values(lse, "lse", rows, dev)
+    _row_values(d_loss, "d_loss", rows, dev)
+    if not (want_dh or want_dw):
+        raise ValueError("dh or dw must be wanted")
+    if add is not None:
+        if not want_dw:
+            raise ValueError("add goes into dw")
+        _dev(add, "add", _FLOATS, 2)
+        if tuple(add.shape) != (vocab, k):
+            raise ValueError("add must have shape %s (got %s)" % ((vocab, k), tuple(add.shape)))
+        _same_device(dev, ("add", add))
+        dw_dtype = add.dtype
+    out = _given(out, "dh", "dw")
+    res = {}
+    if want_dh:
+        t = out.get("dh")
+        if t is None:
+            t = torch.empty((rows, k), dtype=torch.bfloat16, device=dev)
+        else:
+            _out(t, "out dh", (rows, k), torch.bfloat16, dev)
+            _no_overlap(t, "out dh", h, w, targets, lse, d_loss, add)
+        res["dh"] = t
+    if want_dw:
+        t = out.get("dw")
+        if t is None:
+            t = torch.empty((vocab, k), dtype=_out_dtype(dw_dtype), device=dev)
+        else:
+            _out(t, "out dw", (vocab, k), _out_dtype(t.dtype), dev)
+            if add is not None and add.dtype != t.dtype:
+                raise TypeError("add must have dw's dtype %s (got %s)" % (t.dtype, add.dtype))
+            same = add is not None and add.data_ptr() == t.data_ptr()
+            _no_overlap(t, "out dw", h, w, targets, lse, d_loss, None if same else add, res.get("dh"))
+        res["dw"] = t
+    workspace = _workspace(workspace, lib().nvfp4_vocab_loss_backward_workspace(rows, vocab, k), dev, h, w, targets, lse,
+                           d_loss, add, *res.values())
+    dw = res.get("dw")
+    with _on(dev):
+        st = lib().nvfp4_vocab_loss_backward(_ptr(h), _ptr(w), _ptr(targets), _ptr(lse), _ptr(d_loss), rows, vocab, k,
+                                             float(scale), _ptr(add), _ptr(res.get("dh")), _ptr(dw),
+                                             _type(dw), _ptr(workspace), workspace.numel(), _stream(dev))
+    _check("nvfp4_vocab_loss_backward", st)
+    return res

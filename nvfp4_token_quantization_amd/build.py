@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
 SOURCES = ["abi_common.hip", "host_util.hip", "quantize.hip", "swiglu_quantize.hip", "route.hip",
            "dequantize.hip", "mxfp8.hip", "mxfp8_gemm.hip", "gemm.hip", "gemm_skinny.hip",
-           "bf16_gemm.hip", "residual_norm.hip", "moe_combine.hip", "grad_clip.hip"]
+           "bf16_gemm.hip", "residual_norm.hip", "moe_combine.hip", "grad_clip.hip",
+           "moe_gate.hip", "embedding.hip", "vocab_loss.hip"]
 CHECKED_LIB = os.path.join(HERE, "libnvfp4_checked.so")
 CHECKED_SOURCES = SOURCES + ["checks.hip"]
 CHECKED_FLAGS = ("-DNVFP4_CHECKED=1",)

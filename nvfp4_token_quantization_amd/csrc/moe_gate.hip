@@ -1,0 +1,416 @@
+// moe_gate.hip -- the router's gate next to nvfp4_moe_route: the weights of a
+// token's chosen experts, the experts' load and the balance loss, and their
+// gradient (gfx950).
+//
+//   p[t] = softmax(logits[t])
+//   weights[t, j] = p[t, e_j], or p[t, e_j] / sum_j' p[t, e_j'] (normalize)
+//   counts[e] = choices of e, S[e] = sum_t p[t, e], N = tokens that count
+//   loss = E sum_e counts[e] / (sum counts) S[e] / N
+//   dl[t, e] = p[t, e] (c_e - sum_e' p[t, e'] c_e') + the weights' part,
+//     c_e = d_loss E counts[e] / (sum counts N)
+//
+// One pass over the logits each way.  L lanes hold a token, V experts each
+// (expert j + L v), as in the router: a softmax is two exchanges of L lanes in
+// registers.  Forward: a block leaves one row of partial sums of p (lanes over
+// its tokens, then its waves in order) and of counts, added up in block order
+// by one more block, so that nothing depends on the order of atomics; up to
+// one block's tokens, where the call's launches are its time, the block ends
+// the job itself.  Backward: the chosen experts' parts go to the lanes that
+// hold those experts, choice by choice.
+#include <type_traits>
+
+#include "rowwise.h"
+
+namespace nvfp4 {
+
+constexpr int GATE_THREADS = 1024;
+
+struct GateArgs {
+  const float* logits;
+  const int32_t* experts;
+  const uint8_t* valid;  // NULL: every token counts
+  int64_t tokens;
+  int E, K;
+  bool normalize;
+  float* weights;
+  int32_t* counts;   // [E + 1], the last: tokens that count
+  float* prob_sums;  // [E]
+  float* loss;
+  float* part_sums;      // [blocks, E]
+  int32_t* part_counts;  // [blocks, E + 1]
+  const float* d_weights;
+  const float* d_loss;
+  float* d_logits;
+};
+
+// sum or max over aligned groups of L lanes (every lane gets it), a fixed tree
+template <int L, class F>
+__device__ __forceinline__ float group_reduce(float v, F&& f) {
+  v = f(v, __uint_as_float(dpp_mov<0xB1>(__float_as_uint(v))));   // quad_perm [1,0,3,2]
+  v = f(v, __uint_as_float(dpp_mov<0x4E>(__float_as_uint(v))));   // quad_perm [2,3,0,1]
+  v = f(v, __uint_as_float(dpp_mov<0x141>(__float_as_uint(v))));  // row_half_mirror
+  v = f(v, __uint_as_float(dpp_mov<0x140>(__float_as_uint(v))));  // row_mirror
+  if (L >= 32) v = f(v, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F)));
+  if (L >= 64)
+    v = f(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0)),
+          __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32)));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+  return group_reduce<L>(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
+
+// The loss from the summed counts and probabilities of the E experts (thread e
+// holds expert e's; E <= threads), by one block.
+__device__ __forceinline__ void gate_finish(const GateArgs& p, int count, int n, float sum, double (&s)[2][16]) {
+  const int e = threadIdx.x, lane = e & 63;
+  double c = e < p.E ? (double)count : 0.0, cs = e < p.E ? (double)count * (double)sum : 0.0;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    c += __shfl_xor(c, o, 64);
+    cs += __shfl_xor(cs, o, 64);
+  }
+  if (lane == 0) {
+    s[0][e >> 6] = c;
+    s[1][e >> 6] = cs;
+  }
+  if (e < p.E) {
+    p.counts[e] = count;
+    p.prob_sums[e] = sum;
+  }
+  __syncthreads();
+  if (e == 0) {
+    c = cs = 0.0;
+    for (int w = 0; w < GATE_THREADS / 64; ++w) {
+      c += s[0][w];
+      cs += s[1][w];
+    }
+    p.counts[p.E] = n;
+    *p.loss = c > 0.0 ? (float)((double)p.E * cs / (c * (double)n)) : 0.0f;
+  }
+}
+
+// A token's choices: lane j of its group holds choice j + L q in slot q.
+template <int L>
+struct GateChoices {
+  static constexpr int Q = 64 / L;
+  int e[Q];    // -1: none (past K, or an index that is no expert)
+  float x[Q];  // its logit
+};
+template <int L>
+__device__ __forceinline__ void gate_choices(const GateArgs& p, int64_t t, int j, bool ok, GateChoices<L>& c) {
+#pragma unroll
+  for (int q = 0; q < GateChoices<L>::Q; ++q) {
+    const int k = j + L * q;
+    c.e[q] = -1;
+    if (L * q < p.K && ok && k < p.K) {
+      const int e = p.experts[t * p.K + k];
+      if (e >= 0 && e < p.E) c.e[q] = e;
+    }
+    c.x[q] = c.e[q] >= 0 ? p.logits[t * p.E + c.e[q]] : -__builtin_inff();
+  }
+}
+// weights of the choices from the softmax's maximum m and sum s
+template <int L>
+__device__ __forceinline__ void gate_weights(const GateArgs& p, const GateChoices<L>& c, float m, float s,
+                                             float (&w)[GateChoices<L>::Q]) {
+  constexpr int Q = GateChoices<L>::Q;
+  if (p.normalize) {  // a softmax over the chosen, with their own maximum
+    m = c.x[0];
+#pragma unroll
+    for (int q = 1; q < Q; ++q) m = __builtin_fmaxf(m, c.x[q]);
+    m = group_max<L>(m);
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    w[q] = c.e[q] >= 0 ? expf(c.x[q] - m) : 0.0f;
+    sum += w[q];
+  }
+  if (p.normalize) s = group_sum<L>(sum);
+#pragma unroll
+  for (int q = 0; q < Q; ++q) w[q] = c.e[q] >= 0 ? w[q] / s : 0.0f;
+}
+
+// softmax of the token's logits in this lane's experts: p[v] (0 past E)
+template <int L, int V>
+__device__ __forceinline__ void gate_softmax(const GateArgs& p, int64_t t, int j, bool ok, float (&x)[V], float& m,
+                                             float& s) {
+  const float* row = p.logits + t * p.E;
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = ok && j + L * v < p.E ? row[j + L * v] : -__builtin_inff();
+  m = x[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) m = __builtin_fmaxf(m, x[v]);
+  m = group_max<L>(m);
+  s = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    x[v] = j + L * v < p.E ? expf(x[v] - m) : 0.0f;
+    s += x[v];
+  }
+  s = group_sum<L>(s);
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = x[v] / s;
+}
+
+template <int L, int V, bool BALANCE>
+__global__ __launch_bounds__(GATE_THREADS) void gate_kernel(GateArgs p) {
+  constexpr int TPB = GATE_THREADS / L, W = GATE_THREADS / 64;
+  __shared__ float s_sum[BALANCE ? W : 1][L * V];
+  __shared__ int s_cnt[BALANCE ? L * V + 1 : 1];
+  __shared__ double s_fin[2][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, j = lane % L;
+  float acc[V] = {};
+  int n = 0;
+  if (BALANCE) {
+    for (int i = tid; i <= L * V; i += GATE_THREADS) s_cnt[i] = 0;
+    __syncthreads();
+  }
+  for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < p.tokens; t0 += (int64_t)gridDim.x * TPB) {
+    const int64_t t = t0 + tid / L;
+    const bool in = t < p.tokens, ok = in && (!p.valid || p.valid[t]);
+    GateChoices<L> c;
+    gate_choices<L>(p, t, j, ok, c);
+    float x[V], m, s, w[GateChoices<L>::Q];
+    gate_softmax<L, V>(p, t, j, ok, x, m, s);
+    gate_weights<L>(p, c, m, s, w);
+#pragma unroll
+    for (int q = 0; q < GateChoices<L>::Q; ++q) {
+      const int k = j + L * q;
+      if (L * q < p.K && in && k < p.K) p.weights[t * p.K + k] = w[q];
+      if (BALANCE && c.e[q] >= 0) atomicAdd(&s_cnt[c.e[q]], 1);
+    }
+    if (BALANCE && ok) {
+      n += j == 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += x[v];
+    }
+  }
+  if (!BALANCE) return;
+  if (n) atomicAdd(&s_cnt[L * V], n);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int o = L; o < 64; o <<= 1) acc[v] += __shfl_xor(acc[v], o, 64);
+    if (lane < L) s_sum[wave][j + L * v] = acc[v];
+  }
+  __syncthreads();
+  float sum = 0.0f;
+  if (tid < p.E)
+    for (int k = 0; k < W; ++k) sum += s_sum[k][tid];
+  if (gridDim.x == 1) {
+    gate_finish(p, tid < p.E ? s_cnt[tid] : 0, s_cnt[L * V], sum, s_fin);
+    return;
+  }
+  if (tid < p.E) {
+    p.part_sums[(int64_t)blockIdx.x * p.E + tid] = sum;
+    p.part_counts[(int64_t)blockIdx.x * (p.E + 1) + tid] = s_cnt[tid];
+  }
+  if (tid == 0) p.part_counts[(int64_t)blockIdx.x * (p.E + 1) + p.E] = s_cnt[L * V];
+}
+
+// Adds the blocks' partial rows in block order: EP threads (EP >= E + 1, a
+// power of two) take a slice of the blocks each, the slices are added in order.
+__global__ __launch_bounds__(GATE_THREADS) void gate_join_kernel(GateArgs p, int blocks, int EP) {
+  __shared__ float s_sum[GATE_THREADS];
+  __shared__ int s_cnt[GATE_THREADS];
+  __shared__ double s_fin[2][16];
+  const int tid = threadIdx.x, slices = GATE_THREADS / EP, sl = tid / EP, per = (blocks + slices - 1) / slices;
+  // E = 1024 fills the block: its count of tokens is thread 0's extra column
+  const int e = tid % EP, last = min(blocks, (sl + 1) * per);
+  float sum = 0.0f;
+  int cnt = 0, n = 0;
+#pragma unroll 4
+  for (int b = sl * per; b < last; ++b) {
+    if (e < p.E) {
+      sum += p.part_sums[(int64_t)b * p.E + e];
+      cnt += p.part_counts[(int64_t)b * (p.E + 1) + e];
+    }
+    if (e == 0) n += p.part_counts[(int64_t)b * (p.E + 1) + p.E];
+  }
+  s_sum[tid] = sum;
+  s_cnt[tid] = cnt;
+  __syncthreads();
+  if (tid < EP)
+    for (int k = 1; k < slices; ++k) {
+      sum += s_sum[tid + k * EP];
+      cnt += s_cnt[tid + k * EP];
+    }
+  __syncthreads();
+  if (e == 0) s_cnt[sl] = n;
+  __syncthreads();
+  n = 0;
+  for (int k = 0; k < slices; ++k) n += s_cnt[k];
+  gate_finish(p, cnt, n, sum, s_fin);
+}
+
+template <int L, int V>
+__global__ __launch_bounds__(GATE_THREADS) void gate_backward_kernel(GateArgs p) {
+  constexpr int TPB = GATE_THREADS / L, Q = GateChoices<L>::Q;
+  __shared__ unsigned long long s_total;
+  const int tid = threadIdx.x, lane = tid & 63, j = lane % L, base = lane - j;
+  float coef[V] = {};
+  if (p.d_loss) {
+    if (tid == 0) s_total = 0;
+    __syncthreads();
+    if (tid < p.E) atomicAdd(&s_total, (unsigned long long)(long long)p.counts[tid]);
+    __syncthreads();
+    const double c = (double)(long long)s_total, n = (double)p.counts[p.E];
+    const double f = c > 0.0 && n > 0.0 ? (double)*p.d_loss * (double)p.E / (c * n) : 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) coef[v] = j + L * v < p.E ? (float)(f * (double)p.counts[j + L * v]) : 0.0f;
+  }
+  for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < p.tokens; t0 += (int64_t)gridDim.x * TPB) {
+    const int64_t t = t0 + tid / L;
+    const bool in = t < p.tokens, ok = in && (!p.valid || p.valid[t]);
+    float x[V], m, s, up = 0.0f;
+    gate_softmax<L, V>(p, t, j, ok, x, m, s);
+#pragma unroll
+    for (int v = 0; v < V; ++v) up = __builtin_fmaf(x[v], coef[v], up);
+    up = group_sum<L>(up);
+    float g[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = x[v] * (coef[v] - up);
+    if (p.d_weights) {
+      GateChoices<L> c;
+      gate_choices<L>(p, t, j, ok, c);
+      float w[Q], a[Q], dot = 0.0f;
+      gate_weights<L>(p, c, m, s, w);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        a[q] = c.e[q] >= 0 ? p.d_weights[t * p.K + j + L * q] : 0.0f;
+        dot = __builtin_fmaf(w[q], a[q], dot);
+      }
+      dot = group_sum<L>(dot);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) a[q] = p.normalize ? w[q] * (a[q] - dot) : w[q] * a[q];
+      if (!p.normalize) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) g[v] = __builtin_fmaf(-x[v], dot, g[v]);
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int left = min(L, p.K - L * q);
+        for (int k = 0; k < left; ++k) {
+          const int e = __shfl(c.e[q], base + k, 64);
+          const float add = __shfl(a[q], base + k, 64);
+#pragma unroll
+          for (int v = 0; v < V; ++v)
+            if (e == j + L * v) g[v] += add;
+        }
+      }
+    }
+    if (!in) continue;
+    float* row = p.d_logits + t * p.E;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (j + L * v < p.E) row[j + L * v] = ok ? g[v] : 0.0f;
+  }
+}
+
+// Lanes a token and experts a lane, as the router takes them, to `f`.
+template <class F>
+static void gate_shape(int E, F&& f) {
+  if (E <= 16) f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+  else if (E <= 32) f(std::integral_constant<int, 16>(), std::integral_constant<int, 2>());
+  else if (E <= 64) f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
+  else if (E <= 128) f(std::integral_constant<int, 16>(), std::integral_constant<int, 8>());
+  else if (E <= 256) f(std::integral_constant<int, 32>(), std::integral_constant<int, 8>());
+  else if (E <= 512) f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
+  else f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
+}
+
+// blocks of a forward call: a partial row each
+static int64_t gate_blocks(int64_t tokens, int64_t E) {
+  const int64_t tpb = GATE_THREADS / (E <= 128 ? 16 : E <= 256 ? 32 : 64);
+  const int64_t need = (tokens + tpb - 1) / tpb;
+  return need < 1 ? 1 : need < 256 ? need : 256;
+}
+
+}  // namespace nvfp4
+
+using nvfp4host::aligned;
+
+// sizes the calls share
+static int gate_sizes(int64_t tokens, int64_t E, int64_t topk) {
+  if (tokens < 0 || E < 1 || topk < 1 || topk > E) return NVFP4_ERROR_INVALID_VALUE;
+  if (E > 1024 || topk > 64 || tokens * topk >= ((int64_t)1 << 31) || tokens >= ((int64_t)1 << 31))
+    return NVFP4_ERROR_UNSUPPORTED_SHAPE;
+  return NVFP4_SUCCESS;
+}
+
+extern "C" int64_t nvfp4_moe_gate_workspace(int64_t tokens, int64_t num_experts) {
+  if (tokens <= 0 || num_experts < 1) return 0;
+  const int64_t blocks = nvfp4::gate_blocks(tokens, num_experts);
+  return blocks > 1 ? blocks * (2 * num_experts + 1) * 4 : 0;
+}
+
+extern "C" int nvfp4_moe_gate(const float* logits, const int32_t* experts, const uint8_t* valid, int64_t tokens,
+                              int64_t num_experts, int64_t topk, int normalize, float* weights, int32_t* counts,
+                              float* prob_sums, float* loss, void* workspace, int64_t workspace_bytes, void* stream) {
+  int st = gate_sizes(tokens, num_experts, topk);
+  if (st) return st;
+  const bool balance = counts || prob_sums || loss;
+  if (balance && !(counts && prob_sums && loss)) return NVFP4_ERROR_INVALID_VALUE;
+  if (tokens > 0 && (!logits || !experts || !weights)) return NVFP4_ERROR_INVALID_VALUE;
+  const int64_t need = balance ? nvfp4_moe_gate_workspace(tokens, num_experts) : 0;
+  if (workspace_bytes < need || (need > 0 && !workspace)) return NVFP4_ERROR_INVALID_VALUE;
+  if (!aligned(logits, 4) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(counts, 4) ||
+      !aligned(prob_sums, 4) || !aligned(loss, 4) || !aligned(workspace, 4))
+    return NVFP4_ERROR_MISALIGNED;
+  if (tokens == 0 && !balance) return NVFP4_SUCCESS;
+  if ((st = nvfp4host::check_arch())) return st;
+  nvfp4::GateArgs p{};
+  p.logits = logits; p.experts = experts; p.valid = valid; p.tokens = tokens; p.E = (int)num_experts; p.K = (int)topk;
+  p.normalize = normalize != 0; p.weights = weights; p.counts = counts; p.prob_sums = prob_sums; p.loss = loss;
+  const int64_t blocks = nvfp4::gate_blocks(tokens, num_experts);
+  p.part_sums = static_cast<float*>(workspace);
+  p.part_counts = static_cast<int32_t*>(workspace) + blocks * num_experts;
+  hipStream_t str = (hipStream_t)stream;
+  nvfp4::gate_shape(p.E, [&](auto l, auto v) {
+    constexpr int L = decltype(l)::value, V = decltype(v)::value;
+    if (balance)
+      hipLaunchKernelGGL((nvfp4::gate_kernel<L, V, true>), dim3((unsigned)blocks), dim3(nvfp4::GATE_THREADS), 0, str, p);
+    else
+      hipLaunchKernelGGL((nvfp4::gate_kernel<L, V, false>), dim3((unsigned)blocks), dim3(nvfp4::GATE_THREADS), 0, str, p);
+  });
+  if (balance && blocks > 1) {
+    int ep = 1;
+    while (ep < p.E) ep *= 2;
+    hipLaunchKernelGGL(nvfp4::gate_join_kernel, dim3(1), dim3(nvfp4::GATE_THREADS), 0, str, p, (int)blocks, ep);
+  }
+  return nvfp4host::launch_status();
+}
+
+extern "C" int nvfp4_moe_gate_backward(const float* logits, const int32_t* experts, const uint8_t* valid,
+                                       const int32_t* counts, int64_t tokens, int64_t num_experts, int64_t topk,
+                                       int normalize, const float* d_weights, const float* d_loss, float* d_logits,
+                                       void* stream) {
+  int st = gate_sizes(tokens, num_experts, topk);
+  if (st) return st;
+  if (!d_weights && !d_loss) return NVFP4_ERROR_INVALID_VALUE;
+  if (d_loss && !counts) return NVFP4_ERROR_INVALID_VALUE;
+  if (tokens == 0) return NVFP4_SUCCESS;
+  if (!logits || !experts || !d_logits) return NVFP4_ERROR_INVALID_VALUE;
+  if (!aligned(logits, 4) || !aligned(experts, 4) || !aligned(counts, 4) || !aligned(d_weights, 4) ||
+      !aligned(d_loss, 4) || !aligned(d_logits, 4))
+    return NVFP4_ERROR_MISALIGNED;
+  if ((st = nvfp4host::check_arch())) return st;
+  nvfp4::GateArgs p{};
+  p.logits = logits; p.experts = experts; p.valid = valid; p.tokens = tokens; p.E = (int)num_experts; p.K = (int)topk;
+  p.normalize = normalize != 0; p.counts = const_cast<int32_t*>(counts);
+  p.d_weights = d_weights; p.d_loss = d_loss; p.d_logits = d_logits;
+  nvfp4::gate_shape(p.E, [&](auto l, auto v) {
+    constexpr int L = decltype(l)::value, V = decltype(v)::value, TPB = nvfp4::GATE_THREADS / L;
+    const int64_t need = (tokens + TPB - 1) / TPB, cap = (int64_t)nvfp4host::num_cus() * 2;
+    hipLaunchKernelGGL((nvfp4::gate_backward_kernel<L, V>), dim3((unsigned)(need < cap ? need : cap)),
+                       dim3(nvfp4::GATE_THREADS), 0, (hipStream_t)stream, p);
+  });
+  return nvfp4host::launch_status();
+}
