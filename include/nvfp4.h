@@ -593,7 +593,7 @@ int nvfp4_clip_grad_norm(const void* const* grads, void* const* out, const int64
  *   weights  [tokens, topk] f32;  counts [num_experts + 1] i32, prob_sums
  *            [num_experts] f32, loss [1] f32: all three or none.
  *   workspace: nvfp4_moe_gate_workspace(tokens, num_experts) bytes of the
- *            caller's (0 for few tokens), 4-byte aligned, needed for those
+ *            caller's (0 for few tokens), 16-byte aligned, needed for those
  *            three, free for other use when the call's work has completed.
  * Backward: d_logits from d_weights (NULL: no gradient through the weights)
  * and d_loss ([1] f32 device, with the loss's coefficient; NULL: none), at
@@ -607,8 +607,8 @@ int nvfp4_clip_grad_norm(const void* const* grads, void* const* out, const int64
  * <= num_experts, tokens * topk < 2^31.
  * Errors: INVALID_VALUE (sizes, null pointers with work, one or two of the
  * three, a missing or too small workspace, neither d_weights nor d_loss,
- * d_loss without counts), UNSUPPORTED_SHAPE, MISALIGNED (4 bytes), ARCH,
- * LAUNCH.
+ * d_loss without counts), UNSUPPORTED_SHAPE, MISALIGNED (workspace 16 bytes,
+ * the rest 4), ARCH, LAUNCH.
  */
 int64_t nvfp4_moe_gate_workspace(int64_t tokens, int64_t num_experts);
 int nvfp4_moe_gate(const float* logits, const int32_t* experts, const uint8_t* valid, int64_t tokens,

@@ -36,7 +36,7 @@ __device__ __forceinline__ void bg_body(const Bf16Args& p, const BgTile& tl, BgO
                                         uint8_t* block_lds, int nst, int grp, int w, int lane) {
   const int li = lane & 31, h = lane >> 5, wr = w >> 1, wc = w & 1;
   f32x16 acc[VS][TN];
-  if (!bg_sum<MODE, TM, TN, BK, KG, VS>(p, tl, oa, ob, block_lds, nst, grp, w, lane, acc)) return;
+  if (!bg_sum<MODE, TM, TN, BK, KG, VS, 32>(p, tl, oa, ob, block_lds, nst, grp, w, lane, acc)) return;
 
   // Epilogue through LDS, slab by slab, in a region of this wave's own: 16
   // bytes a lane and whole row segments per store instruction.

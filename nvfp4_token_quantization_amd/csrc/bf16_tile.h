@@ -3,6 +3,9 @@
 // the vocabulary loss differ in their schedules and in what they do with a tile.
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "gemm_common.h"
 #include "rowwise.h"
 
@@ -48,6 +51,13 @@ __device__ __forceinline__ int bg_row_swz(int r) {
 template <int TN>
 __device__ __forceinline__ int bg_col_swz(int r) {
   return TN == 1 ? (r & 2) << 1 : ((r & 3) << 2) ^ (r & 2);
+}
+
+// The same for 16 x 16 x 32 fragments, whose lanes 16 .. 31 read rows 8 further
+// on: those take the other 32 bytes of each 64.
+template <int TN>
+__device__ __forceinline__ int bg_col_swz16(int r) {
+  return (TN == 1 ? (r & 2) << 1 : (r & 3) << 2) ^ ((r >> 2) & 2);
 }
 
 template <int MODE> struct BgMode {
@@ -98,6 +108,47 @@ __device__ __forceinline__ bf16x8 bg_frag_cols(uint8_t* st, int sl, int t, int l
   return __builtin_bit_cast(bf16x8, v);
 }
 
+// The same for v_mfma_f32_16x16x32_bf16: 16 rows or columns (half `sub` of slab
+// `sl`), summed elements [32 t + 8 q, +8) for lane 16 q + i.
+template <int BK>
+__device__ __forceinline__ bf16x8 bg_frag16_rows(const uint8_t* st, int sl, int sub, int t, int lane) {
+  const int i = lane & 15, chunk = (4 * t + (lane >> 4)) ^ bg_row_swz<BK>(i);
+  return *reinterpret_cast<const bf16x8*>(st + sl * (64 * BK) + (16 * sub + i) * (2 * BK) + chunk * 16);
+}
+template <int T>
+__device__ __forceinline__ bf16x8 bg_frag16_cols(uint8_t* st, int sl, int sub, int t, int lane) {
+  const int i = lane & 15, r4 = i >> 2;
+  const int row = 32 * t + 8 * (lane >> 4) + r4;
+  const int chunk = (4 * sl + 2 * sub + ((i & 3) >> 1)) ^ bg_col_swz16<T>(row);
+  uint8_t* p = st + row * (128 * T) + chunk * 16 + (i & 1) * 8;
+  typedef __attribute__((address_space(3))) s16x4* lds4;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * 128 * T));
+  const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// f(0), f(1), .. f(N - 1) with constants: unrolled whatever the size of f
+template <int... I, class F>
+__device__ __forceinline__ void static_for_each(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_each(std::make_integer_sequence<int, N>(), f);
+}
+
+// MFMA shapes: 32 x 32 x 16 (F = 1) and 16 x 16 x 32 (F = 2 fragments a slab).
+template <int SH> struct BgShape;
+template <> struct BgShape<32> {
+  typedef f32x16 acc;
+  static constexpr int F = 1, KS = 16;
+};
+template <> struct BgShape<16> {
+  typedef f32x4 acc;
+  static constexpr int F = 2, KS = 32;
+};
+
 // Blocks of a tile shape that share a CU's 160 KiB, and the LDS each gets:
 // the stage ring, and for a gathered wgrad each wave's ring of row indices.
 template <int TM, int TN>
@@ -123,9 +174,11 @@ constexpr int bg_bufs(int bytes) {
 // free.  p: the arguments' row_index and a_rows.
 template <int VS, int TN, int KG>
 constexpr int bg_sums() { return (KG - 1) * 4 * VS * TN * 16 * 64 * 4; }  // the other groups' accumulators
-template <int MODE, int TM, int TN, int BK, int KG, int VS, class Args>
+template <int MODE, int TM, int TN, int BK, int KG, int VS, int SH, class Args>
 __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperand<TM>& oa, BgOperand<TN>& ob,
-                                       uint8_t* block_lds, int nst, int grp, int w, int lane, f32x16 (&acc)[VS][TN]) {
+                                       uint8_t* block_lds, int nst, int grp, int w, int lane,
+                                       typename BgShape<SH>::acc (&acc)[BgShape<SH>::F * VS][BgShape<SH>::F * TN]) {
+  constexpr int F = BgShape<SH>::F, FA = F * VS, FN = F * TN, READS = FA + FN;
   uint8_t* lds = block_lds + (KG > 1 ? grp * (160 * 1024 / KG) : 0);
   typedef BgMode<MODE> M;
   constexpr int TA = M::a_cols ? TM : VS;  // A slabs of a stage
@@ -134,7 +187,7 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
   constexpr int NB = bg_bufs<MODE, TM, TN, KG>(STAGE);
   static_assert(NB >= 2, "a stage in use and one in flight");
   constexpr int AT = NA * 4096;  // the stage's B follows its A
-  constexpr int NT = BK / 16;    // MFMA steps of a stage
+  constexpr int NT = BK / BgShape<SH>::KS;  // MFMA steps of a stage
   const int li = lane & 31, h = lane >> 5, wr = w >> 1, wc = w & 1;
   const uint32_t lbase = (uint32_t)(uintptr_t)lds;
   const bool gather = MODE == BG_WGRAD && p.row_index != nullptr;
@@ -147,7 +200,7 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
   };
   // this lane's rows of its DMAs of B in a stage, from the ring
   constexpr int RPI = 8 / TN;  // summed rows an instruction covers
-  auto gather_rows = [&](int s, int32_t (&idx)[NC - NA]) {
+  auto gather_rows = [&](int s, int32_t (&idx)[NC - NA]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NC - NA; ++i) {
       const int r = (4 * i + w) * RPI + lane / (8 * TN);
@@ -164,7 +217,7 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
   };
   constexpr int CPR = BK / 8;  // chunks of a row operand's LDS row
   const int chunk8 = 8 * ((lane % CPR) ^ bg_row_swz<BK>(64 / CPR * w + lane / CPR));
-  auto issue_at = [&](int s, int buf) {
+  auto issue_at = [&](int s, int buf) __attribute__((always_inline)) {
     Issue q;
     q.s = s;
     q.at = lbase + (uint32_t)buf * STAGE + (uint32_t)w * 1024;
@@ -175,7 +228,7 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
     q.rb = M::b_cols && !gather ? bg_rsrc(ob.base + (int64_t)s * BK * ob.stride, left * ob.stride) : ob.rsrc;
     return q;
   };
-  auto issue_one = [&](const Issue& q, const int32_t (&idx)[NC - NA], int k) {
+  auto issue_one = [&](const Issue& q, const int32_t (&idx)[NC - NA], int k) __attribute__((always_inline)) {
     if (k < NA) {
       if constexpr (M::a_cols) dma16(q.ra, oa.voff[k], 0, q.at + k * 4096);
       else dma16(q.ra, q.in ? oa.voff[k] : BG_OOB, q.soff, q.at + k * 4096);
@@ -194,31 +247,68 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
     }
   };
   // fragment k (A slabs, then B slabs) of MFMA step t of the stage in buffer buf
-  auto read_one = [&](int buf, int t, bf16x8 (&fa)[VS], bf16x8 (&fb)[TN], int k) {
+  auto read_at = [&](uint8_t* st, uint8_t* sb, int t, bf16x8 (&fa)[FA], bf16x8 (&fb)[FN], int k) __attribute__((always_inline)) {
+    if constexpr (SH == 32) {
+      if (k < VS)
+        fa[k] = M::a_cols ? bg_frag_cols<TM>(st, 2 * k + wr, t, lane) : bg_frag_rows<BK>(st, 2 * k + wr, t, li, h);
+      else
+        fb[k - VS] = M::b_cols ? bg_frag_cols<TN>(sb, TN * wc + k - VS, t, lane)
+                               : bg_frag_rows<BK>(sb, TN * wc + k - VS, t, li, h);
+    } else {
+      if (k < FA) {
+        const int sl = 2 * (k / F) + wr;
+        fa[k] = M::a_cols ? bg_frag16_cols<TM>(st, sl, k % F, t, lane) : bg_frag16_rows<BK>(st, sl, k % F, t, lane);
+      } else {
+        const int sl = TN * wc + (k - FA) / F;
+        fb[k - FA] = M::b_cols ? bg_frag16_cols<TN>(sb, sl, (k - FA) % F, t, lane)
+                               : bg_frag16_rows<BK>(sb, sl, (k - FA) % F, t, lane);
+      }
+    }
+  };
+  auto read_one = [&](int buf, int t, bf16x8 (&fa)[FA], bf16x8 (&fb)[FN], int k) __attribute__((always_inline)) {
     uint8_t* st = lds + buf * STAGE;
-    if (k < VS)
-      fa[k] = M::a_cols ? bg_frag_cols<TM>(st, 2 * k + wr, t, lane) : bg_frag_rows<BK>(st, 2 * k + wr, t, li, h);
-    else
-      fb[k - VS] = M::b_cols ? bg_frag_cols<TN>(st + AT, TN * wc + k - VS, t, lane)
-                             : bg_frag_rows<BK>(st + AT, TN * wc + k - VS, t, li, h);
+    read_at(st, st + AT, t, fa, fb, k);
   };
 #pragma unroll
-  for (int i = 0; i < VS; ++i)
+  for (int i = 0; i < FA; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = (f32x16){0};
+    for (int j = 0; j < FN; ++j) acc[i][j] = (typename BgShape<SH>::acc){0};
   // The MFMAs of one step with `items` other instructions spread among them,
   // pinned in this order: the matrix pipe never waits for a burst of LDS
   // reads or DMAs to issue.
-  auto mma = [&](const bf16x8 (&fa)[VS], const bf16x8 (&fb)[TN], int items, auto&& item) {
-    constexpr int S = VS * TN;
+  auto mma = [&](const bf16x8 (&fa)[FA], const bf16x8 (&fb)[FN], int items, auto&& item) {
+    constexpr int S = FA * FN;
 #pragma unroll
     for (int m = 0; m < S; ++m) {
-      const int i = m / TN, j = m % TN;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      const int i = m / FN, j = m % FN;
+      if constexpr (SH == 32) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      else acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
 #pragma unroll
       for (int k = m * items / S; k < (m + 1) * items / S; ++k) item(k);
       __builtin_amdgcn_sched_barrier(0);
     }
+  };
+
+  // The same with the reads among the first three quarters of the MFMAs, so that
+  // none is waited for at the step's end, B before A: row i of A is dead after
+  // its MFMAs, so that the next step's A takes its registers over.
+  auto mma_early = [&](const bf16x8 (&fa)[FA], const bf16x8 (&fb)[FN], auto&& read, auto dmas, auto&& dma) __attribute__((always_inline)) {
+    constexpr int S = FA * FN, H = S * 3 / 4, DMAS = decltype(dmas)::value;
+    static_for<S>([&](auto mc) __attribute__((always_inline)) {
+      constexpr int m = decltype(mc)::value, i = m / FN, j = m % FN;
+      if constexpr (SH == 32) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      else acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      if constexpr (m < H) {
+        constexpr int k0 = m * READS / H, k1 = (m + 1) * READS / H;
+        static_for<k1 - k0>([&](auto k) __attribute__((always_inline)) {
+          constexpr int r = k0 + decltype(k)::value;
+          read(r < FN ? FA + r : r - FN);
+        });
+      }
+      constexpr int d0 = m * DMAS / S, d1 = (m + 1) * DMAS / S;
+      static_for<d1 - d0>([&](auto k) __attribute__((always_inline)) { dma(d0 + decltype(k)::value); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
 
   int32_t idx[NC - NA] = {};
@@ -235,22 +325,54 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
   }
   // Fragments are read LOOK MFMA steps ahead: two where a step has few MFMAs,
   // which would not cover the LDS latency.
-  constexpr int LOOK = VS <= 2 && NT == 4 ? 2 : 1, FB = 2 * LOOK;
-  bf16x8 fa[FB][VS], fb[FB][TN];
+  constexpr int LOOK = SH == 32 && VS <= 2 && NT == 4 ? 2 : 1, FB = 2 * LOOK;
+  bf16x8 fa[FB][FA], fb[FB][FN];
   if (gather) wait_vmcnt<(NB - 1) * (NC + 1)>();
   else wait_vmcnt<(NB - 1) * NC>();
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
   for (int t = 0; t < LOOK; ++t)
 #pragma unroll
-    for (int k = 0; k < VS + TN; ++k) read_one(0, t, fa[t], fb[t], k);
+    for (int k = 0; k < READS; ++k) read_one(0, t, fa[t], fb[t], k);
   int cur = 0;
+  // Stage s, whose first fragments are in set `first`; leaves those of the next
+  // stage in set `first + NT` (of two).
+  auto stage = [&](auto set, int s) __attribute__((always_inline)) {
+    constexpr int SET = decltype(set)::value;
+    const int nxt = cur + 1 == NB ? 0 : cur + 1;
+    if (gather) gather_rows(s + NB, idx);
+#pragma unroll
+    for (int t = 0; t < NT - 1; ++t)
+      mma_early(fa[(SET + t) & 1], fb[(SET + t) & 1],
+                [&](int k) __attribute__((always_inline)) { read_one(cur, t + 1, fa[(SET + t + 1) & 1], fb[(SET + t + 1) & 1], k); }, std::integral_constant<int, 0>(), [](int) {});
+    wait_lgkmcnt0();
+    if (gather) wait_vmcnt<(NB - 2) * (NC + 1)>();
+    else wait_vmcnt<(NB - 2) * NC>();
+    asm volatile("s_barrier" ::: "memory");
+    const Issue q = issue_at(s + NB, cur);
+    mma_early(fa[(SET + NT - 1) & 1], fb[(SET + NT - 1) & 1],
+              [&](int k) __attribute__((always_inline)) { read_one(nxt, 0, fa[(SET + NT) & 1], fb[(SET + NT) & 1], k); }, std::integral_constant<int, NC>(),
+              [&](int k) __attribute__((always_inline)) { issue_one(q, idx, k); });
+    if (gather) issue_index(s + 2 * NB);
+    cur = nxt;
+  };
+  constexpr std::integral_constant<int, 0> s0{};
+  if constexpr (SH == 16 && NT % 2 == 0) {
+    for (int s = 0; s < nst; ++s) stage(s0, s);
+  } else if constexpr (SH == 16) {  // the two sets change places from stage to stage
+    constexpr std::integral_constant<int, 1> s1{};
+    // an odd last stage is followed by one past the sum, which adds zeros
+    for (int s = 0; s < nst; s += 2) {
+      stage(s0, s);
+      stage(s1, s + 1);
+    }
+  } else
   for (int s = 0; s < nst; ++s) {
     const int nxt = cur + 1 == NB ? 0 : cur + 1;
     if (gather) gather_rows(s + NB, idx);
 #pragma unroll
     for (int t = 0; t < NT - LOOK; ++t)
-      mma(fa[t % FB], fb[t % FB], VS + TN,
+      mma(fa[t % FB], fb[t % FB], READS,
           [&](int k) { read_one(cur, t + LOOK, fa[(t + LOOK) % FB], fb[(t + LOOK) % FB], k); });
     // every read of stage s has landed and stage s + 1 is there: after the
     // barrier, for all four waves
@@ -262,9 +384,9 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
 #pragma unroll
     for (int u = 0; u < LOOK; ++u) {
       const int t = NT - LOOK + u, d0 = NC * u / LOOK, d1 = NC * (u + 1) / LOOK;
-      mma(fa[t % FB], fb[t % FB], VS + TN + d1 - d0, [&](int k) {
-        if (k < VS + TN) read_one(nxt, u, fa[u], fb[u], k);
-        else issue_one(q, idx, d0 + k - VS - TN);
+      mma(fa[t % FB], fb[t % FB], READS + d1 - d0, [&](int k) {
+        if (k < READS) read_one(nxt, u, fa[u], fb[u], k);
+        else issue_one(q, idx, d0 + k - READS);
       });
     }
     if (gather) issue_index(s + 2 * NB);
@@ -274,6 +396,7 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
   wait_vmcnt<0>();
   asm volatile("s_barrier" ::: "memory");
   if constexpr (KG > 1) {
+    static_assert(SH == 32, "only this shape's accumulators are laid out here");
     float* sums = reinterpret_cast<float*>(block_lds);
 #pragma unroll
     for (int i = 0; i < VS; ++i)

@@ -19,12 +19,14 @@
 //     Other blocks of the same launch meanwhile write the table rows that no
 //     token names (zeros, or add; nothing when the sum goes in place).
 //  4. embed_join_kernel adds the partial rows of a run that crosses.
+#include <type_traits>
+
 #include "rowwise.h"
 
 namespace nvfp4 {
 
 constexpr int EMBED_CHUNK = 2048;  // ids sorted together
-constexpr int EMBED_RANK = 64;     // ids a block of step 1 places, by 4 slices of the chunk
+constexpr int EMBED_RANK = 64;     // ids a block of step 1 places, by 16 slices of the chunk
 constexpr int EMBED_MERGE = 128;   // ids a block of step 2 places, by 8 slices of the chunks
 constexpr int EMBED_ROWS = 64;     // table rows a block looks for and fills
 constexpr uint32_t EMBED_NONE = 0x7FFFFFFFu;  // an id outside the table: sorted last
@@ -52,54 +54,142 @@ __device__ __forceinline__ uint32_t embed_key(const EmbedArgs& p, int64_t i) {
   return id >= 0 && id < p.vocab ? (uint32_t)id : EMBED_NONE;
 }
 
-template <bool VEC>
+// How a lane holds 8 of a wave's 512 columns: C consecutive ones at a time, C =
+// 8 (16 bytes of bf16), 4 (16 bytes of fp32) or 1 (rows of odd width or address).
+// Accesses go through a resource over the row: columns past its end read as
+// zeros and are not written, without a branch, so that the loads of several
+// rows are in flight together.
+template <int C>
+__device__ __forceinline__ uint32_t embed_col(int piece, int g, int lane) {
+  return (uint32_t)(512 * piece + 64 * C * g + C * lane);
+}
+template <int C, bool BF>
+__device__ __forceinline__ void embed_load(const void* row, int64_t d, int piece, int lane, float (&o)[8]) {
+  const __amdgpu_buffer_rsrc_t r = row_rsrc(row, BF, d);
+#pragma unroll
+  for (int g = 0; g < 8 / C; ++g) {
+    const uint32_t at = embed_col<C>(piece, g, lane) * (BF ? 2 : 4);
+    float* v = o + C * g;
+    if constexpr (C == 1) {
+      if constexpr (BF) v[0] = bf16_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0));
+      else v[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+    } else if constexpr (BF) {
+      uint32_t u[C / 2];
+      if constexpr (C == 8) {
+        const u32x4 q = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+        for (int i = 0; i < 4; ++i) u[i] = q[i];
+      } else {
+        const auto q = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+        for (int i = 0; i < 2; ++i) u[i] = q[i];
+      }
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < C / 4; ++h) {
+        const u32x4 q = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 * h, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * h + i] = __uint_as_float(q[i]);
+      }
+    }
+  }
+}
+// rounded once when BF; streaming stores (AUX = 2) for what is not read again soon
+template <int C, bool BF, int AUX>
+__device__ __forceinline__ void embed_store(void* row, int64_t d, int piece, int lane, const float (&o)[8]) {
+  const __amdgpu_buffer_rsrc_t r = row_rsrc(row, BF, d);
+#pragma unroll
+  for (int g = 0; g < 8 / C; ++g) {
+    const uint32_t at = embed_col<C>(piece, g, lane) * (BF ? 2 : 4);
+    const float* v = o + C * g;
+    if constexpr (C == 1) {
+      if constexpr (BF) __builtin_amdgcn_raw_buffer_store_b16(to_bf16(v[0]), r, at, 0, AUX);
+      else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, at, 0, AUX);
+    } else if constexpr (BF) {
+      if constexpr (C == 8) {
+        const u32x4 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+        __builtin_amdgcn_raw_buffer_store_b128(w, r, at, 0, AUX);
+      } else {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(w, r, at, 0, AUX);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < C / 4; ++h) {
+        const u32x4 w = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                         __float_as_uint(v[4 * h + 3])};
+        __builtin_amdgcn_raw_buffer_store_b128(w, r, at + 16 * h, 0, AUX);
+      }
+    }
+  }
+}
+
+template <int C, bool IN_BF, bool OUT_BF>
 __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs p) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t items = p.tokens * p.pieces;
-  for (int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); item < items; item += (int64_t)gridDim.x * 4) {
+  for (int64_t item = (int64_t)blockIdx.x * 4 + wave; item < items; item += (int64_t)gridDim.x * 4) {
     const int64_t t = item / p.pieces;
     const int piece = (int)(item % p.pieces);
     const int32_t id = p.ids[t];
     float v[8] = {};
     if (id >= 0 && id < p.vocab) {
-      load8<VEC>(row_at(p.in, p.in_bf, id, p.d), p.in_bf, p.d, piece, 64, lane, v);
+      embed_load<C, IN_BF>(row_at(p.in, IN_BF, id, p.d), p.d, piece, lane, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= p.scale;
     }
-    store8<VEC>(row_at(p.out, p.out_bf, t, p.d), p.out_bf, p.d, piece, 64, lane, v);
+    embed_store<C, OUT_BF, 2>(row_at(p.out, OUT_BF, t, p.d), p.d, piece, lane, v);
   }
 }
 
-__global__ __launch_bounds__(256) void embed_rank_kernel(EmbedArgs p) {
+__global__ __launch_bounds__(1024) void embed_rank_kernel(EmbedArgs p) {
+  constexpr int SLICES = 16, PER = EMBED_CHUNK / SLICES, PARTS = EMBED_CHUNK / EMBED_RANK;
   __shared__ __attribute__((aligned(16))) uint32_t s_key[EMBED_CHUNK];
-  __shared__ int s_rank[4][EMBED_RANK];
-  const int tid = threadIdx.x, lane = tid & 63, slice = tid >> 6;
-  constexpr int PARTS = EMBED_CHUNK / EMBED_RANK;
+  __shared__ int s_rank[SLICES][EMBED_RANK];
+  const int tid = threadIdx.x, lane = tid & 63, slice = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t c0 = (int64_t)(blockIdx.x / PARTS) * EMBED_CHUNK;
-  const int own = (int)(blockIdx.x % PARTS) * EMBED_RANK + lane;  // within the chunk
+  const int part = (int)(blockIdx.x % PARTS) * EMBED_RANK, own = part + lane;  // within the chunk
   const int n = (int)min((int64_t)EMBED_CHUNK, p.tokens - c0);
-  for (int i = tid; i < EMBED_CHUNK; i += 256) s_key[i] = i < n ? embed_key(p, c0 + i) : 0xFFFFFFFFu;  // goes before none
+  for (int i = tid; i < EMBED_CHUNK; i += 1024) s_key[i] = i < n ? embed_key(p, c0 + i) : 0xFFFFFFFFu;  // goes before none
   __syncthreads();
   const uint32_t mine = s_key[own];
-  const int per = EMBED_CHUNK / 4;
+  const int lo = slice * PER;
   int rank = 0;
-  const uint4* q = reinterpret_cast<const uint4*>(s_key + slice * per);
+  const uint4* q = reinterpret_cast<const uint4*>(s_key + lo);
+  if (lo <= part && part < lo + PER) {
+    // the block's own tokens are among the slice: an equal id goes before when its token does
 #pragma unroll 4
-  for (int i = 0; i < per / 4; ++i) {
-    const uint4 k = q[i];
-    const int at = slice * per + 4 * i;
-    // equal ids go before when their token does
-    rank += k.x < mine + (at < own);
-    rank += k.y < mine + (at + 1 < own);
-    rank += k.z < mine + (at + 2 < own);
-    rank += k.w < mine + (at + 3 < own);
+    for (int i = 0; i < PER / 4; ++i) {
+      const uint4 k = q[i];
+      const int at = lo + 4 * i;
+      rank += k.x < mine + (at < own);
+      rank += k.y < mine + (at + 1 < own);
+      rank += k.z < mine + (at + 2 < own);
+      rank += k.w < mine + (at + 3 < own);
+    }
+  } else {
+    const uint32_t limit = mine + (lo < part);  // equal ids all go before, or none does
+#pragma unroll 8
+    for (int i = 0; i < PER / 4; ++i) {
+      const uint4 k = q[i];
+      rank += k.x < limit;
+      rank += k.y < limit;
+      rank += k.z < limit;
+      rank += k.w < limit;
+    }
   }
   s_rank[slice][lane] = rank;
   __syncthreads();
   if (slice == 0 && own < n) {
-    const int64_t at = c0 + s_rank[0][lane] + s_rank[1][lane] + s_rank[2][lane] + s_rank[3][lane];
-    p.key[0][at] = mine;
-    p.pos[0][at] = (int32_t)(c0 + own);
+    int at = 0;
+#pragma unroll
+    for (int k = 0; k < SLICES; ++k) at += s_rank[k][lane];
+    p.key[0][c0 + at] = mine;
+    p.pos[0][c0 + at] = (int32_t)(c0 + own);
   }
 }
 
@@ -152,38 +242,45 @@ __device__ __forceinline__ int64_t embed_lower(const EmbedArgs& p, uint32_t id) 
 }
 
 // table row v = add[v] + scale * sum
-template <bool VEC>
+template <int C, bool OUT_BF>
 __device__ __forceinline__ void embed_write(const EmbedArgs& p, uint32_t v, int piece, int lane, const float (&sum)[8]) {
   float o[8] = {};
-  if (p.add) load8<VEC>(row_at(p.add, p.out_bf, v, p.d), p.out_bf, p.d, piece, 64, lane, o);
+  if (p.add) embed_load<C, OUT_BF>(row_at(p.add, OUT_BF, v, p.d), p.d, piece, lane, o);
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = p.add ? __builtin_fmaf(p.scale, sum[i], o[i]) : p.scale * sum[i];
-  store8<VEC>(row_at(p.out, p.out_bf, v, p.d), p.out_bf, p.d, piece, 64, lane, o);
+  embed_store<C, OUT_BF, 2>(row_at(p.out, OUT_BF, v, p.d), p.d, piece, lane, o);
+}
+
+// Table rows [v0, v0 + EMBED_ROWS) that no token names: zeros, or add.
+template <bool WIDE>
+__device__ __forceinline__ void embed_fill(const EmbedArgs& p, int64_t v0, int tid) {
+  const int lane = tid & 63;
+  const int64_t v = v0 + lane;
+  const int64_t at = v < p.vocab ? embed_lower(p, (uint32_t)v) : p.tokens;
+  const bool named = v >= p.vocab || (at < p.tokens && p.key[p.sorted][at] == (uint32_t)v);
+  uint64_t fill = ~__ballot(named);
+  typedef typename std::conditional<WIDE, u32x4, uint16_t>::type word;
+  const int64_t n = p.d * (p.out_bf ? 2 : 4) / (int64_t)sizeof(word);  // of a row
+  const word* add = static_cast<const word*>(p.add);
+  word* out = static_cast<word*>(p.out);
+  while (fill) {
+    const int64_t row = v0 + __builtin_ctzll(fill);
+    fill &= fill - 1;
+    for (int64_t i = row * n + tid; i < (row + 1) * n; i += 256)
+      __builtin_nontemporal_store(add ? __builtin_nontemporal_load(add + i) : word{}, out + i);
+  }
 }
 
 constexpr int EMBED_AHEAD = 8;  // rows in flight
 
-template <bool VEC>
+template <int C, bool IN_BF, bool OUT_BF, bool WIDE>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs p, int64_t sum_blocks) {
   const int tid = threadIdx.x, lane = tid & 63;
   if (blockIdx.x >= sum_blocks) {
-    // table rows that no token names
-    const int64_t v0 = (int64_t)(blockIdx.x - sum_blocks) * EMBED_ROWS, v = v0 + lane;
-    const int64_t at = v < p.vocab ? embed_lower(p, (uint32_t)v) : p.tokens;
-    const bool named = v >= p.vocab || (at < p.tokens && p.key[p.sorted][at] == (uint32_t)v);
-    uint64_t fill = ~__ballot(named);
-    while (fill) {
-      const int r = __builtin_ctzll(fill);
-      fill &= fill - 1;
-      for (int piece = tid >> 6; piece < p.pieces; piece += 4) {
-        float o[8] = {};
-        if (p.add) load8<VEC>(row_at(p.add, p.out_bf, v0 + r, p.d), p.out_bf, p.d, piece, 64, lane, o);
-        store8<VEC>(row_at(p.out, p.out_bf, v0 + r, p.d), p.out_bf, p.d, piece, 64, lane, o);
-      }
-    }
+    embed_fill<WIDE>(p, (int64_t)(blockIdx.x - sum_blocks) * EMBED_ROWS, tid);
     return;
   }
-  const int64_t item = (int64_t)blockIdx.x * 4 + (tid >> 6);
+  const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t b = item / p.pieces;
   const int piece = (int)(item % p.pieces);
   if (b >= p.runs) return;
@@ -194,17 +291,16 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs p, int64_t sum
   const uint32_t my_key = lane < n ? key[i0 + lane] : EMBED_NONE;
   const int32_t my_pos = lane < n ? pos[i0 + lane] : 0;
   const uint32_t prev = i0 > 0 ? key[i0 - 1] : EMBED_NONE, next = i1 < p.tokens ? key[i1] : EMBED_NONE;
-  const uint64_t live = __ballot(my_key != EMBED_NONE);  // the first `count` lanes
-  const int count = __popcll(live);
+  const int count = __popcll(__ballot(my_key != EMBED_NONE));  // ids of the table come first
   float sum[8] = {};
   for (int g = 0; g < count; g += EMBED_AHEAD) {
     float v[EMBED_AHEAD][8];
 #pragma unroll
-    for (int k = 0; k < EMBED_AHEAD; ++k)
-      if (g + k < count) {
-        const int32_t t = __builtin_amdgcn_readlane(my_pos, g + k);
-        load8<VEC>(row_at(p.in, p.in_bf, t, p.d), p.in_bf, p.d, piece, 64, lane, v[k]);
-      }
+    for (int k = 0; k < EMBED_AHEAD; ++k) {
+      // past the last: that one again, into nothing
+      const int32_t t = __builtin_amdgcn_readlane(my_pos, min(g + k, count - 1));
+      embed_load<C, IN_BF>(row_at(p.in, IN_BF, t, p.d), p.d, piece, lane, v[k]);
+    }
 #pragma unroll
     for (int k = 0; k < EMBED_AHEAD; ++k) {
       if (g + k >= count) break;
@@ -217,9 +313,9 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs p, int64_t sum
       // the id's run ends here, or goes on past this wave's tokens
       const bool from_before = id == prev, goes_on = after == id;
       if (from_before || goes_on)
-        store8<VEC>(p.part + (2 * b + (from_before ? 0 : 1)) * p.d, false, p.d, piece, 64, lane, sum);
+        embed_store<C, false, 0>(p.part + (2 * b + (from_before ? 0 : 1)) * p.d, p.d, piece, lane, sum);
       else
-        embed_write<VEC>(p, id, piece, lane, sum);
+        embed_write<C, OUT_BF>(p, id, piece, lane, sum);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
     }
@@ -228,26 +324,30 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs p, int64_t sum
 
 // Block (b, piece): the run that starts in b's tokens and goes on past them.
 constexpr int EMBED_JOIN = 8;  // waves that share the partial rows
-template <bool VEC>
+template <int C, bool OUT_BF>
 __global__ __launch_bounds__(64 * EMBED_JOIN) void embed_join_kernel(EmbedArgs p) {
   __shared__ float s_sum[EMBED_JOIN][8][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t b = blockIdx.x / p.pieces;
   const int piece = (int)(blockIdx.x % p.pieces);
   const uint32_t* key = p.key[p.sorted];
-  const int64_t i0 = b * p.run, i1 = i0 + p.run;  // i1 <= tokens: the last block is not launched
+  const int64_t i0 = b * p.run, i1 = i0 + p.run;  // i1 < tokens: the last block is not launched
   const uint32_t id = key[i1 - 1];
   if (id == EMBED_NONE || key[i1] != id || (i0 > 0 && key[i0 - 1] == id)) return;  // block-uniform
   const int64_t last = (embed_lower(p, id + 1) - 1) / p.run;  // block of its last token
   float sum[8] = {};
-  if (wave == 0) load8<VEC>(p.part + (2 * b + 1) * p.d, false, p.d, piece, 64, lane, sum);
+  if (wave == 0) embed_load<C, false>(p.part + (2 * b + 1) * p.d, p.d, piece, lane, sum);
   const int64_t rows = last - b, per = (rows + EMBED_JOIN - 1) / EMBED_JOIN, end = min(rows, (wave + 1) * per);
-#pragma unroll 4
-  for (int64_t k = wave * per; k < end; ++k) {
-    float v[8];
-    load8<VEC>(p.part + 2 * (b + 1 + k) * p.d, false, p.d, piece, 64, lane, v);
+  for (int64_t g = wave * per; g < end; g += EMBED_AHEAD) {
+    float v[EMBED_AHEAD][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] += v[e];
+    for (int k = 0; k < EMBED_AHEAD; ++k)
+      embed_load<C, false>(p.part + 2 * (b + 1 + min(g + k, end - 1)) * p.d, p.d, piece, lane, v[k]);
+#pragma unroll
+    for (int k = 0; k < EMBED_AHEAD; ++k)
+      if (g + k < end)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[k][e];
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) s_sum[wave][e][lane] = sum[e];
@@ -256,11 +356,19 @@ __global__ __launch_bounds__(64 * EMBED_JOIN) void embed_join_kernel(EmbedArgs p
   for (int w = 1; w < EMBED_JOIN; ++w)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] += s_sum[w][e][lane];
-  embed_write<VEC>(p, id, piece, lane, sum);
+  embed_write<C, OUT_BF>(p, id, piece, lane, sum);
 }
 
-static bool embed_vec(int64_t d, const void* a, const void* b, const void* c) {
-  return d % 8 == 0 && nvfp4host::aligned(a, 16) && nvfp4host::aligned(b, 16) && nvfp4host::aligned(c, 16);
+// rows of `d` elements that lie on 16-byte (bf16: C = 4, 8-byte) pieces of C elements
+static bool embed_pieces(int64_t d, int C, const void* a, const void* b, const void* c) {
+  return d % C == 0 && nvfp4host::aligned(a, 16) && nvfp4host::aligned(b, 16) && nvfp4host::aligned(c, 16);
+}
+template <class F>
+static void embed_types(bool in_bf, bool out_bf, F&& f) {
+  if (in_bf && out_bf) f(std::true_type(), std::true_type());
+  else if (in_bf) f(std::true_type(), std::false_type());
+  else if (out_bf) f(std::false_type(), std::true_type());
+  else f(std::false_type(), std::false_type());
 }
 
 // Sorted tokens a wave adds: 64 at most (its lanes hold their ids), and fewer
@@ -306,10 +414,14 @@ extern "C" int nvfp4_embedding(const void* table, int table_type, int64_t vocab,
   p.pieces = (int)((d + 511) / 512);
   const int64_t blocks = (tokens * p.pieces + 3) / 4;
   const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
-  if (nvfp4::embed_vec(d, table, out, nullptr))
-    hipLaunchKernelGGL(nvfp4::embed_kernel<true>, grid, dim3(256), 0, (hipStream_t)stream, p);
-  else
-    hipLaunchKernelGGL(nvfp4::embed_kernel<false>, grid, dim3(256), 0, (hipStream_t)stream, p);
+  nvfp4::embed_types(p.in_bf, p.out_bf, [&](auto in, auto o) {
+    constexpr bool IN = decltype(in)::value, OUT = decltype(o)::value;
+    constexpr int WIDE = IN && OUT ? 8 : 4;
+    if (nvfp4::embed_pieces(d, WIDE, table, out, nullptr))
+      hipLaunchKernelGGL((nvfp4::embed_kernel<WIDE, IN, OUT>), grid, dim3(256), 0, (hipStream_t)stream, p);
+    else
+      hipLaunchKernelGGL((nvfp4::embed_kernel<1, IN, OUT>), grid, dim3(256), 0, (hipStream_t)stream, p);
+  });
   return nvfp4host::launch_status();
 }
 
@@ -351,7 +463,7 @@ extern "C" int nvfp4_embedding_backward(const void* dout, int dout_type, const i
   if (tokens > 0) {
     // blocks of ids that exist (the last chunk may be short)
     const int64_t parts = (tokens + nvfp4::EMBED_RANK - 1) / nvfp4::EMBED_RANK;
-    hipLaunchKernelGGL(nvfp4::embed_rank_kernel, dim3((unsigned)parts), dim3(256), 0, str, p);
+    hipLaunchKernelGGL(nvfp4::embed_rank_kernel, dim3((unsigned)parts), dim3(1024), 0, str, p);
     if (chunks > 1)
       hipLaunchKernelGGL(nvfp4::embed_merge_kernel, dim3((unsigned)((tokens + nvfp4::EMBED_MERGE - 1) / nvfp4::EMBED_MERGE)),
                          dim3(1024), 0, str, p);
@@ -359,12 +471,18 @@ extern "C" int nvfp4_embedding_backward(const void* dout, int dout_type, const i
   const int64_t sum_blocks = (p.runs * p.pieces + 3) / 4;
   const int64_t fill_blocks = add == dtable ? 0 : (vocab + nvfp4::EMBED_ROWS - 1) / nvfp4::EMBED_ROWS;
   const dim3 grid((unsigned)(sum_blocks + fill_blocks)), join((unsigned)((p.runs - 1) * p.pieces));
-  if (nvfp4::embed_vec(d, dout, dtable, add)) {
-    hipLaunchKernelGGL(nvfp4::embed_sum_kernel<true>, grid, dim3(256), 0, str, p, sum_blocks);
-    if (p.runs > 1) hipLaunchKernelGGL(nvfp4::embed_join_kernel<true>, join, dim3(64 * nvfp4::EMBED_JOIN), 0, str, p);
-  } else {
-    hipLaunchKernelGGL(nvfp4::embed_sum_kernel<false>, grid, dim3(256), 0, str, p, sum_blocks);
-    if (p.runs > 1) hipLaunchKernelGGL(nvfp4::embed_join_kernel<false>, join, dim3(64 * nvfp4::EMBED_JOIN), 0, str, p);
-  }
+  const bool wide = d * (p.out_bf ? 2 : 4) % 16 == 0 && aligned(dtable, 16) && aligned(add, 16);
+  nvfp4::embed_types(p.in_bf, p.out_bf, [&](auto in, auto o) {
+    constexpr bool IN = decltype(in)::value, OUT = decltype(o)::value;
+    auto launch = [&](auto c, auto w) {
+      constexpr int C = decltype(c)::value;
+      hipLaunchKernelGGL((nvfp4::embed_sum_kernel<C, IN, OUT, decltype(w)::value>), grid, dim3(256), 0, str, p, sum_blocks);
+      if (p.runs > 1)
+        hipLaunchKernelGGL((nvfp4::embed_join_kernel<C, OUT>), join, dim3(64 * nvfp4::EMBED_JOIN), 0, str, p);
+    };
+    if (wide && nvfp4::embed_pieces(d, 4, dout, dtable, add)) launch(std::integral_constant<int, 4>(), std::true_type());
+    else if (wide) launch(std::integral_constant<int, 1>(), std::true_type());
+    else launch(std::integral_constant<int, 1>(), std::false_type());
+  });
   return nvfp4host::launch_status();
 }

@@ -36,8 +36,12 @@ struct GateArgs {
   int32_t* counts;   // [E + 1], the last: tokens that count
   float* prob_sums;  // [E]
   float* loss;
-  float* part_sums;      // [blocks, E]
-  int32_t* part_counts;  // [blocks, E + 1]
+  // a block's partial row: E sums of p, then E counts, each padded to EP = 4
+  // ceil(E / 4); after the rows the tokens that each block counted
+  float* part_sums;      // [blocks, EP]
+  int32_t* part_counts;  // [blocks, EP]
+  int32_t* part_tokens;  // [blocks]
+  int EP;
   const float* d_weights;
   const float* d_loss;
   float* d_logits;
@@ -102,18 +106,27 @@ struct GateChoices {
   int e[Q];    // -1: none (past K, or an index that is no expert)
   float x[Q];  // its logit
 };
-template <int L>
-__device__ __forceinline__ void gate_choices(const GateArgs& p, int64_t t, int j, bool ok, GateChoices<L>& c) {
+// Loads of a group's token t (any token of the call for a group without one):
+// logits of the lane's experts, its choices, whether the token counts.  All
+// are issued before the first is looked at.
+template <int L, int V>
+__device__ __forceinline__ bool gate_load(const GateArgs& p, int64_t t, int j, bool in, float (&x)[V], GateChoices<L>& c) {
+  const float* row = p.logits + t * p.E;
+#pragma unroll
+  for (int v = 0; v < V; ++v) x[v] = row[min(j + L * v, p.E - 1)];
+#pragma unroll
+  for (int q = 0; q < GateChoices<L>::Q; ++q) c.e[q] = L * q < p.K ? p.experts[t * p.K + min(j + L * q, p.K - 1)] : -1;
+  const bool ok = in && (!p.valid || p.valid[t]);
 #pragma unroll
   for (int q = 0; q < GateChoices<L>::Q; ++q) {
-    const int k = j + L * q;
-    c.e[q] = -1;
-    if (L * q < p.K && ok && k < p.K) {
-      const int e = p.experts[t * p.K + k];
-      if (e >= 0 && e < p.E) c.e[q] = e;
-    }
-    c.x[q] = c.e[q] >= 0 ? p.logits[t * p.E + c.e[q]] : -__builtin_inff();
+    if (!ok || j + L * q >= p.K || c.e[q] < 0 || c.e[q] >= p.E) c.e[q] = -1;
+    c.x[q] = L * q < p.K ? row[max(c.e[q], 0)] : 0.0f;
+    if (c.e[q] < 0) c.x[q] = -__builtin_inff();
   }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (j + L * v >= p.E) x[v] = -__builtin_inff();
+  return ok;
 }
 // weights of the choices from the softmax's maximum m and sum s
 template <int L>
@@ -137,13 +150,9 @@ __device__ __forceinline__ void gate_weights(const GateArgs& p, const GateChoice
   for (int q = 0; q < Q; ++q) w[q] = c.e[q] >= 0 ? w[q] / s : 0.0f;
 }
 
-// softmax of the token's logits in this lane's experts: p[v] (0 past E)
+// the lane's logits x to their softmax over the token's (0 past E)
 template <int L, int V>
-__device__ __forceinline__ void gate_softmax(const GateArgs& p, int64_t t, int j, bool ok, float (&x)[V], float& m,
-                                             float& s) {
-  const float* row = p.logits + t * p.E;
-#pragma unroll
-  for (int v = 0; v < V; ++v) x[v] = ok && j + L * v < p.E ? row[j + L * v] : -__builtin_inff();
+__device__ __forceinline__ void gate_softmax(const GateArgs& p, int j, float (&x)[V], float& m, float& s) {
   m = x[0];
 #pragma unroll
   for (int v = 1; v < V; ++v) m = __builtin_fmaxf(m, x[v]);
@@ -174,11 +183,11 @@ __global__ __launch_bounds__(GATE_THREADS) void gate_kernel(GateArgs p) {
   }
   for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < p.tokens; t0 += (int64_t)gridDim.x * TPB) {
     const int64_t t = t0 + tid / L;
-    const bool in = t < p.tokens, ok = in && (!p.valid || p.valid[t]);
+    const bool in = t < p.tokens;
     GateChoices<L> c;
-    gate_choices<L>(p, t, j, ok, c);
     float x[V], m, s, w[GateChoices<L>::Q];
-    gate_softmax<L, V>(p, t, j, ok, x, m, s);
+    const bool ok = gate_load<L, V>(p, in ? t : 0, j, in, x, c);
+    gate_softmax<L, V>(p, j, x, m, s);
     gate_weights<L>(p, c, m, s, w);
 #pragma unroll
     for (int q = 0; q < GateChoices<L>::Q; ++q) {
@@ -208,69 +217,90 @@ __global__ __launch_bounds__(GATE_THREADS) void gate_kernel(GateArgs p) {
     gate_finish(p, tid < p.E ? s_cnt[tid] : 0, s_cnt[L * V], sum, s_fin);
     return;
   }
-  if (tid < p.E) {
-    p.part_sums[(int64_t)blockIdx.x * p.E + tid] = sum;
-    p.part_counts[(int64_t)blockIdx.x * (p.E + 1) + tid] = s_cnt[tid];
+  if (tid < p.EP) {  // past E: zeros
+    p.part_sums[(int64_t)blockIdx.x * p.EP + tid] = sum;
+    p.part_counts[(int64_t)blockIdx.x * p.EP + tid] = tid < p.E ? s_cnt[tid] : 0;
   }
-  if (tid == 0) p.part_counts[(int64_t)blockIdx.x * (p.E + 1) + p.E] = s_cnt[L * V];
+  if (tid == 0) p.part_tokens[blockIdx.x] = s_cnt[L * V];
 }
 
-// Adds the blocks' partial rows in block order: EP threads (EP >= E + 1, a
-// power of two) take a slice of the blocks each, the slices are added in order.
-__global__ __launch_bounds__(GATE_THREADS) void gate_join_kernel(GateArgs p, int blocks, int EP) {
-  __shared__ float s_sum[GATE_THREADS];
-  __shared__ int s_cnt[GATE_THREADS];
+// Adds the blocks' partial rows, four columns a thread: the threads of a row
+// are a slice, a slice takes every `slices`-th row in order (eight in flight),
+// and the slices are added in order.
+__global__ __launch_bounds__(GATE_THREADS) void gate_join_kernel(GateArgs p, int blocks) {
+  __shared__ __attribute__((aligned(16))) float s_sum[4 * GATE_THREADS];
+  __shared__ __attribute__((aligned(16))) int s_cnt[4 * GATE_THREADS];
+  __shared__ int s_n[GATE_THREADS / 64];
   __shared__ double s_fin[2][16];
-  const int tid = threadIdx.x, slices = GATE_THREADS / EP, sl = tid / EP, per = (blocks + slices - 1) / slices;
-  // E = 1024 fills the block: its count of tokens is thread 0's extra column
-  const int e = tid % EP, last = min(blocks, (sl + 1) * per);
-  float sum = 0.0f;
-  int cnt = 0, n = 0;
-#pragma unroll 4
-  for (int b = sl * per; b < last; ++b) {
-    if (e < p.E) {
-      sum += p.part_sums[(int64_t)b * p.E + e];
-      cnt += p.part_counts[(int64_t)b * (p.E + 1) + e];
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  const int tid = threadIdx.x, width = p.EP / 4, slices = GATE_THREADS / width, sl = tid / width, col = 4 * (tid % width);
+  int n = tid < blocks ? p.part_tokens[tid] : 0;  // blocks <= GATE_THREADS
+  f32x4 sum = {0, 0, 0, 0};
+  i32x4 cnt = {0, 0, 0, 0};
+  if (sl < slices) {
+    for (int b0 = sl; b0 < blocks; b0 += 8 * slices) {
+      f32x4 a[8];
+      i32x4 c[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t at = (int64_t)min(b0 + k * slices, blocks - 1) * p.EP + col;
+        a[k] = *reinterpret_cast<const f32x4*>(p.part_sums + at);
+        c[k] = *reinterpret_cast<const i32x4*>(p.part_counts + at);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (b0 + k * slices < blocks) {
+          sum += a[k];
+          cnt += c[k];
+        }
     }
-    if (e == 0) n += p.part_counts[(int64_t)b * (p.E + 1) + p.E];
+    *reinterpret_cast<f32x4*>(s_sum + sl * p.EP + col) = sum;
+    *reinterpret_cast<i32x4*>(s_cnt + sl * p.EP + col) = cnt;
   }
-  s_sum[tid] = sum;
-  s_cnt[tid] = cnt;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o, 64);
+  if ((tid & 63) == 0) s_n[tid >> 6] = n;
   __syncthreads();
-  if (tid < EP)
-    for (int k = 1; k < slices; ++k) {
-      sum += s_sum[tid + k * EP];
-      cnt += s_cnt[tid + k * EP];
+  float total = 0.0f;
+  int choices = 0;
+  if (tid < p.E)
+    for (int k = 0; k < slices; ++k) {
+      total += s_sum[k * p.EP + tid];
+      choices += s_cnt[k * p.EP + tid];
     }
-  __syncthreads();
-  if (e == 0) s_cnt[sl] = n;
-  __syncthreads();
   n = 0;
-  for (int k = 0; k < slices; ++k) n += s_cnt[k];
-  gate_finish(p, cnt, n, sum, s_fin);
+  for (int k = 0; k < GATE_THREADS / 64; ++k) n += s_n[k];
+  gate_finish(p, choices, n, total, s_fin);
 }
 
 template <int L, int V>
 __global__ __launch_bounds__(GATE_THREADS) void gate_backward_kernel(GateArgs p) {
   constexpr int TPB = GATE_THREADS / L, Q = GateChoices<L>::Q;
-  __shared__ unsigned long long s_total;
   const int tid = threadIdx.x, lane = tid & 63, j = lane % L, base = lane - j;
-  float coef[V] = {};
-  if (p.d_loss) {
-    if (tid == 0) s_total = 0;
-    __syncthreads();
-    if (tid < p.E) atomicAdd(&s_total, (unsigned long long)(long long)p.counts[tid]);
-    __syncthreads();
-    const double c = (double)(long long)s_total, n = (double)p.counts[p.E];
-    const double f = c > 0.0 && n > 0.0 ? (double)*p.d_loss * (double)p.E / (c * n) : 0.0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) coef[v] = j + L * v < p.E ? (float)(f * (double)p.counts[j + L * v]) : 0.0f;
-  }
-  for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < p.tokens; t0 += (int64_t)gridDim.x * TPB) {
+  float coef[V] = {}, x[V], m, s;
+  GateChoices<L> c;
+  bool ok = false;
+  for (int64_t t0 = (int64_t)blockIdx.x * TPB, first = 1; t0 < p.tokens; t0 += (int64_t)gridDim.x * TPB, first = 0) {
     const int64_t t = t0 + tid / L;
-    const bool in = t < p.tokens, ok = in && (!p.valid || p.valid[t]);
-    float x[V], m, s, up = 0.0f;
-    gate_softmax<L, V>(p, t, j, ok, x, m, s);
+    const bool in = t < p.tokens;
+    ok = gate_load<L, V>(p, in ? t : 0, j, in, x, c);
+    if (first && p.d_loss) {  // while the first token's loads are on their way
+      int k[V];
+      double all = 0.0;  // a sum of whole numbers: exact
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        k[v] = p.counts[min(j + L * v, p.E)];
+        all += j + L * v < p.E ? (double)k[v] : 0.0;
+      }
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) all += __shfl_xor(all, o, 64);
+      const double n = (double)p.counts[p.E];
+      const double f = all > 0.0 && n > 0.0 ? (double)*p.d_loss * (double)p.E / (all * n) : 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) coef[v] = j + L * v < p.E ? (float)(f * (double)k[v]) : 0.0f;
+    }
+    float up = 0.0f;
+    gate_softmax<L, V>(p, j, x, m, s);
 #pragma unroll
     for (int v = 0; v < V; ++v) up = __builtin_fmaf(x[v], coef[v], up);
     up = group_sum<L>(up);
@@ -278,13 +308,11 @@ __global__ __launch_bounds__(GATE_THREADS) void gate_backward_kernel(GateArgs p)
 #pragma unroll
     for (int v = 0; v < V; ++v) g[v] = x[v] * (coef[v] - up);
     if (p.d_weights) {
-      GateChoices<L> c;
-      gate_choices<L>(p, t, j, ok, c);
       float w[Q], a[Q], dot = 0.0f;
       gate_weights<L>(p, c, m, s, w);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        a[q] = c.e[q] >= 0 ? p.d_weights[t * p.K + j + L * q] : 0.0f;
+        a[q] = c.e[q] >= 0 ? p.d_weights[t * p.K + j + L * q] : 0.0f;  // of no choice: read into nothing
         dot = __builtin_fmaf(w[q], a[q], dot);
       }
       dot = group_sum<L>(dot);
@@ -348,7 +376,7 @@ static int gate_sizes(int64_t tokens, int64_t E, int64_t topk) {
 extern "C" int64_t nvfp4_moe_gate_workspace(int64_t tokens, int64_t num_experts) {
   if (tokens <= 0 || num_experts < 1) return 0;
   const int64_t blocks = nvfp4::gate_blocks(tokens, num_experts);
-  return blocks > 1 ? blocks * (2 * num_experts + 1) * 4 : 0;
+  return blocks > 1 ? blocks * (2 * ((num_experts + 3) / 4 * 4) + 1) * 4 : 0;
 }
 
 extern "C" int nvfp4_moe_gate(const float* logits, const int32_t* experts, const uint8_t* valid, int64_t tokens,
@@ -362,7 +390,7 @@ extern "C" int nvfp4_moe_gate(const float* logits, const int32_t* experts, const
   const int64_t need = balance ? nvfp4_moe_gate_workspace(tokens, num_experts) : 0;
   if (workspace_bytes < need || (need > 0 && !workspace)) return NVFP4_ERROR_INVALID_VALUE;
   if (!aligned(logits, 4) || !aligned(experts, 4) || !aligned(weights, 4) || !aligned(counts, 4) ||
-      !aligned(prob_sums, 4) || !aligned(loss, 4) || !aligned(workspace, 4))
+      !aligned(prob_sums, 4) || !aligned(loss, 4) || !aligned(workspace, 16))
     return NVFP4_ERROR_MISALIGNED;
   if (tokens == 0 && !balance) return NVFP4_SUCCESS;
   if ((st = nvfp4host::check_arch())) return st;
@@ -371,7 +399,9 @@ extern "C" int nvfp4_moe_gate(const float* logits, const int32_t* experts, const
   p.normalize = normalize != 0; p.weights = weights; p.counts = counts; p.prob_sums = prob_sums; p.loss = loss;
   const int64_t blocks = nvfp4::gate_blocks(tokens, num_experts);
   p.part_sums = static_cast<float*>(workspace);
-  p.part_counts = static_cast<int32_t*>(workspace) + blocks * num_experts;
+  p.EP = (p.E + 3) / 4 * 4;
+  p.part_counts = static_cast<int32_t*>(workspace) + blocks * p.EP;
+  p.part_tokens = p.part_counts + blocks * p.EP;
   hipStream_t str = (hipStream_t)stream;
   nvfp4::gate_shape(p.E, [&](auto l, auto v) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value;
@@ -380,11 +410,8 @@ extern "C" int nvfp4_moe_gate(const float* logits, const int32_t* experts, const
     else
       hipLaunchKernelGGL((nvfp4::gate_kernel<L, V, false>), dim3((unsigned)blocks), dim3(nvfp4::GATE_THREADS), 0, str, p);
   });
-  if (balance && blocks > 1) {
-    int ep = 1;
-    while (ep < p.E) ep *= 2;
-    hipLaunchKernelGGL(nvfp4::gate_join_kernel, dim3(1), dim3(nvfp4::GATE_THREADS), 0, str, p, (int)blocks, ep);
-  }
+  if (balance && blocks > 1)
+    hipLaunchKernelGGL(nvfp4::gate_join_kernel, dim3(1), dim3(nvfp4::GATE_THREADS), 0, str, p, (int)blocks);
   return nvfp4host::launch_status();
 }
 

@@ -7,9 +7,9 @@
 //   dh = dz w,  dw = add + dz^T h
 //
 // Rows without a target (t_r outside the vocabulary) are taken out first: a
-// scan numbers the others, and every product runs over those alone, gathered
-// from h by that numbering, so that prompt and padding rows cost nothing and
-// whatever they hold reaches no gradient.
+// scan numbers the others, their h is copied together, and every product runs
+// over those alone, so that prompt and padding rows cost nothing and whatever
+// they hold reaches no gradient.
 //
 // Forward: the block tiles of the bf16 products, with an epilogue that leaves
 // one partial sum a row and tile.  The sums are taken relative to a reference
@@ -39,12 +39,13 @@ struct VocabArgs {
   const int32_t* targets;
   int64_t rows, vocab, k;
   float scale;
-  // workspace: number of the rows that have a target, the row of each number,
-  // the number of each row (-1: none), and by number
+  // workspace: how many rows have a target, the row of each number, the number
+  // of each row (-1: none), and by number
   int32_t *count, *row_index, *number;
-  int32_t* target;   // its target
+  int32_t* target;   // backward: its target
   float* ref;        // forward: scale log2(e) <h, w_t>; backward: lse log2(e)
   float* coef;       // backward: scale d_loss
+  uint16_t* hc;      // its h
   float2* part;      // forward: [tiles][rows] exponent and sum of a tile
   float *loss, *lse;
   // backward
@@ -68,409 +69,498 @@ __device__ __forceinline__ bool has_target(const VocabArgs& p, int64_t r) {
   return t >= 0 && t < p.vocab;
 }
 
-// Block 0 numbers the rows with a target in order; the other blocks (forward)
-// take the targets' logits, a wave a row, into ref by row.
-__global__ __launch_bounds__(1024) void vocab_rows_kernel(VocabArgs p) {
-  __shared__ int s_wave[16];
+// One block numbers the rows with a target in order, 8 rows a thread.
+__global__ __launch_bounds__(1024) void vocab_number_kernel(VocabArgs p) {
+  __shared__ int s_wave[2][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (blockIdx.x > 0) {
-    for (int64_t r = (int64_t)(blockIdx.x - 1) * 16 + wave; r < p.rows; r += (int64_t)(gridDim.x - 1) * 16) {
-      const int32_t t = p.targets[r];
-      if (t < 0 || t >= p.vocab) continue;
-      float acc = 0.0f;
-      for (int64_t e = 8 * lane; e < p.k; e += 512) {
-        float a[8], b[8];
-        load8<true>(p.h + r * p.k + e, true, 8, 0, 64, 0, a);
-        load8<true>(p.w + (int64_t)t * p.k + e, true, 8, 0, 64, 0, b);
+  int base = 0, turn = 0;
+  for (int64_t r0 = 0; r0 < p.rows; r0 += 8192, turn ^= 1) {
+    const int64_t r = r0 + 8 * tid;
+    uint32_t has = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(a[i], b[i], acc);
-      }
-      acc = wave_sum_f32(acc);
-      if (lane == 0) p.ref[r] = acc * (p.scale * LOG2E);
+    for (int i = 0; i < 8; ++i) {
+      const int32_t t = p.targets[min(r + i, p.rows - 1)];
+      has |= (uint32_t)(r + i < p.rows && t >= 0 && t < p.vocab) << i;
     }
-    return;
-  }
-  int base = 0;
-  for (int64_t r0 = 0; r0 < p.rows; r0 += 1024) {
-    const int64_t r = r0 + tid;
-    const bool has = r < p.rows && has_target(p, r);
-    const uint64_t b = __ballot(has);
-    if (lane == 0) s_wave[wave] = __popcll(b);
+    const int mine = __popc(has), incl = wave_incl_scan(mine);
+    if (lane == 63) s_wave[turn][wave] = incl;
     __syncthreads();
-    int at = base, total = 0;
+    int at = base + incl - mine, total = 0;
     for (int w = 0; w < 16; ++w) {
-      if (w < wave) at += s_wave[w];
-      total += s_wave[w];
+      if (w < wave) at += s_wave[turn][w];
+      total += s_wave[turn][w];
     }
-    at += __popcll(b & ((1ull << lane) - 1));
-    if (r < p.rows) {
-      if (p.number) p.number[r] = has ? at : -1;
-      if (has) {
-        p.row_index[at] = (int32_t)r;
-        if (p.coef) {
-          p.target[at] = p.targets[r];
-          p.ref[at] = p.lse_in[r] * LOG2E;
-          p.coef[at] = p.d_loss[r] * p.scale;
-        }
-      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = (has >> i) & 1u;
+      if (p.number && r + i < p.rows) p.number[r + i] = in ? at : -1;
+      if (in) p.row_index[at++] = (int32_t)(r + i);
     }
     base += total;
-    __syncthreads();
   }
   if (tid == 0) *p.count = base;
 }
 
-// ------------------------------------------------------------------ tiles --
-
-// Tile (m, n) of a grid of tm x tn for block b of it: block b runs on XCD
-// b % 8, an XCD takes an eighth of the tiles in order, and the order goes
-// through bands of up to 8 tiles along m, m fastest, so that the tiles an XCD
-// works on at a time share panels of both operands in its L2.
-__device__ __forceinline__ bool vocab_tile(int64_t tm, int64_t tn, int64_t b, int64_t& m, int64_t& n) {
-  const int64_t x = b % 8, j = b / 8, tiles = tm * tn;
-  const int64_t lo = tiles * x / 8, hi = tiles * (x + 1) / 8;
-  if (lo + j >= hi) return false;
-  const int64_t t = lo + j, band = t / (8 * tn), in = t % (8 * tn), bh = min((int64_t)8, tm - 8 * band);
-  m = 8 * band + in % bh;
-  n = in / bh;
-  return true;
+// A wave a numbered row: its h, and forward its target's logit, backward its
+// target, lse and coefficient.  FEW rows (up to 1024): a wave a row, numbered
+// here, since another launch would take longer than every block's own count.
+constexpr int FEW_ROWS = 1024;
+template <bool FORWARD, bool FEW>
+__global__ __launch_bounds__(256) void vocab_rows_kernel(VocabArgs p) {
+  __shared__ int s_sum[2][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int64_t i, end, r = 0;
+  if (FEW) {
+    int has = 0;  // of rows 4 tid .. + 3; the block's own are those of thread blockIdx.x
+#pragma unroll
+    for (int c = 0; c < 4; ++c) has += 4 * tid + c < p.rows && has_target(p, min((int64_t)(4 * tid + c), p.rows - 1));
+    const int before = wave_sum_i32(tid < (int)blockIdx.x ? has : 0), all = wave_sum_i32(has);
+    if (lane == 0) {
+      s_sum[0][wave] = before;
+      s_sum[1][wave] = all;
+    }
+    __syncthreads();
+    i = s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3];
+    if (blockIdx.x == 0 && tid == 0) *p.count = s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
+    r = 4 * (int64_t)blockIdx.x + wave;
+    if (r >= p.rows) return;
+    const bool mine = has_target(p, r);
+    for (int c = 0; c < wave; ++c) i += has_target(p, r - wave + c);
+    if (lane == 0) {
+      if (p.number) p.number[r] = mine ? (int32_t)i : -1;
+      if (mine) p.row_index[i] = (int32_t)r;
+    }
+    if (!mine) return;
+    end = i + 1;
+  } else {
+    i = (int64_t)blockIdx.x * 4 + wave;
+    end = *p.count;
+  }
+  for (; i < end; i += (int64_t)gridDim.x * 4) {
+    if (!FEW) r = p.row_index[i];
+    const int32_t t = p.targets[r];
+    const uint4* h = reinterpret_cast<const uint4*>(p.h + r * p.k);
+    const uint4* w = reinterpret_cast<const uint4*>(p.w + (int64_t)t * p.k);
+    uint4* to = reinterpret_cast<uint4*>(p.hc + i * p.k);
+    float acc = 0.0f;
+#pragma unroll 4
+    for (int64_t e = lane; e < p.k / 8; e += 64) {
+      const uint4 a = h[e];
+      to[e] = a;
+      if (FORWARD) {
+        const uint4 b = w[e];
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc = __builtin_fmaf(__uint_as_float(u[c] << 16), __uint_as_float(v[c] << 16), acc);
+          acc = __builtin_fmaf(__uint_as_float(u[c] & 0xFFFF0000u), __uint_as_float(v[c] & 0xFFFF0000u), acc);
+        }
+      }
+    }
+    if (FORWARD) {
+      acc = wave_sum_f32(acc);
+      if (lane == 0) p.ref[i] = acc * (p.scale * LOG2E);
+    } else if (lane == 0) {
+      p.target[i] = t;
+      p.ref[i] = p.lse_in[r] * LOG2E;
+      p.coef[i] = p.d_loss[r] * p.scale;
+    }
+  }
 }
 
-// Row operand: DMA offsets of T slabs of rows [row0, rows) of a matrix whose
-// rows are `rowb` bytes, from the resource's base; `index`: gathered rows.
+// ------------------------------------------------------------- tile order --
+
+// Tile t of a grid of tm x tn: the order goes through bands of up to 8 tiles
+// along m, m fastest, so that the tiles that an XCD works on at a time share
+// panels of both operands in its L2.
+__device__ __forceinline__ void vocab_tile(int64_t tm, int64_t tn, int64_t t, int64_t& m, int64_t& n) {
+  // at most 2^28 tiles; quotients come from the vector unit, so say that they are uniform
+  const uint32_t row = 8 * (uint32_t)tn, band = __builtin_amdgcn_readfirstlane((uint32_t)t / row);
+  const uint32_t in = (uint32_t)t - band * row, bh = min(8u, (uint32_t)tm - 8 * band);
+  const uint32_t q = __builtin_amdgcn_readfirstlane(in / bh);
+  m = 8 * band + (in - q * bh);
+  n = q;
+}
+// The block's tile: each XCD (block b runs on XCD b % 8) takes an eighth of the
+// tiles in order.  False: none.
+__device__ __forceinline__ bool vocab_turn(int64_t tiles, int64_t& t) {
+  const int64_t x = blockIdx.x % 8;
+  t = ((tiles * x) >> 3) + blockIdx.x / 8;
+  return t < ((tiles * (x + 1)) >> 3);
+}
+
+// ------------------------------------------------------ what tiles leave --
+
+// sum or max over aligned groups of 16 lanes (every lane gets it)
+template <class F>
+__device__ __forceinline__ float reduce16(float v, F&& f) {
+  v = f(v, __uint_as_float(dpp_mov<0xB1>(__float_as_uint(v))));      // quad_perm [1,0,3,2]
+  v = f(v, __uint_as_float(dpp_mov<0x4E>(__float_as_uint(v))));      // quad_perm [2,3,0,1]
+  v = f(v, __uint_as_float(dpp_mov<0x141>(__float_as_uint(v))));     // row_half_mirror
+  return f(v, __uint_as_float(dpp_mov<0x140>(__float_as_uint(v))));  // row_mirror
+}
+__device__ __forceinline__ float sum16(float v) {
+  return reduce16(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float max16(float v) {
+  return reduce16(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
+
+// Sums of a tile by v_mfma_f32_16x16x32_bf16: acc[a][b][r] of lane 16 q + c is
+// row 32 (2 (a / 2) + wr) + 16 (a % 2) + 4 q + r, column 32 TN wc + 16 b + c of
+// the tile, for wave 2 wr + wc of four.
+template <int VS, int TN>
+using Acc = f32x4[2 * VS][2 * TN];
+
+// One row of the tile by each thread: its reference, coefficient and target.
+struct RowTerms {
+  float ref, coef;
+  int col;  // the target's column in the tile, -1: none of it
+};
+template <bool DZ>
+__device__ __forceinline__ RowTerms row_terms(const VocabArgs& p, int64_t row, int64_t row_hi, int64_t col0, int cols) {
+  RowTerms o = {0.0f, 0.0f, -1};
+  if (row >= row_hi) return o;
+  o.ref = p.ref[row];
+  if (DZ) {
+    o.coef = p.coef[row];
+    const int64_t c = (int64_t)p.target[row] - p.v0 - col0;
+    o.col = c >= 0 && c < cols ? (int)c : -1;
+  }
+  return o;
+}
+
+// Partial sums of the tile's rows over its columns, relative to the rows'
+// references (s_ref, of the tile's rows): exponent and sum to p.part[n].  s_part:
+// LDS for 2 x 64 TM of them.
+template <int VS, int TM, int TN>
+__device__ __forceinline__ void tile_part(const VocabArgs& p, const Acc<VS, TN>& acc, const float* s_ref, float2* s_part,
+                                          int64_t row_lo, int64_t row_hi, int64_t n, int w, int lane) {
+  constexpr int BM = 64 * TM, BN = 64 * TN;
+  const int c16 = lane & 15, q16 = lane >> 4, wr = w >> 1, wc = w & 1;
+  const float f = p.scale * LOG2E;
+  const int left = (int)min((int64_t)BN, p.width - n * BN) - 32 * TN * wc - c16;  // this lane's column of b exists: 16 b < left
+  const bool whole = p.width - n * BN >= BN;
+#pragma unroll
+  for (int a = 0; a < 2 * VS; ++a) {
+    const int row0 = 32 * (2 * (a / 2) + wr) + 16 * (a % 2) + 4 * q16;
+    const f32x4 ref = *reinterpret_cast<const f32x4*>(s_ref + row0);
+    float s[4] = {}, top[4];
+    bool over = false;
+    auto sum = [&](auto all) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int b = 0; b < 2 * TN; ++b) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[a][b][r], f, -ref[r]));
+          s[r] += decltype(all)::value || 16 * b < left ? e : 0.0f;
+        }
+    };
+    if (whole) sum(std::true_type());
+    else sum(std::false_type());
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      top[r] = ref[r];
+      s[r] = sum16(s[r]);
+      over |= !(s[r] < 0x1p120f);
+    }
+    if (__ballot(over)) {  // wave-uniform: such a row's sum relative to its maximum here
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float t = -__builtin_inff(), u = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 2 * TN; ++b) t = 16 * b < left ? __builtin_fmaxf(t, acc[a][b][r] * f) : t;
+        t = max16(t);
+#pragma unroll
+        for (int b = 0; b < 2 * TN; ++b) {
+          const float z = acc[a][b][r] * f;
+          u += 16 * b < left && z != -__builtin_inff() ? __builtin_amdgcn_exp2f(z - t) : 0.0f;
+        }
+        u = sum16(u);
+        // of this row alone: its neighbours keep their bits
+        if (!(s[r] < 0x1p120f)) {
+          s[r] = u;
+          top[r] = t;
+        }
+      }
+    }
+    if (c16 == 0) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s_part[wc * BM + row0 + r] = make_float2(top[r], s[r]);
+    }
+  }
+  __syncthreads();
+  for (int r = threadIdx.x; r < 64 * VS; r += 256) {
+    if (row_lo + r >= row_hi) continue;
+    const float2 a0 = s_part[r], a1 = s_part[BM + r];
+    float2 o = make_float2(__builtin_fmaxf(a0.x, a1.x), 0.0f);
+    if (a0.x == a1.x) o.y = a0.y + a1.y;
+    else o.y = a0.y * __builtin_amdgcn_exp2f(a0.x - o.x) + a1.y * __builtin_amdgcn_exp2f(a1.x - o.x);
+    p.part[n * p.rows + row_lo + r] = o;
+  }
+}
+
+// dz of the tile, 16 rows of a wave at a time: columns of 16 rows go to LDS (TN
+// KiB a wave) 8 bytes a lane and come back as rows (ds_read_b64_tr_b16), 16 bytes
+// a lane.  Columns past the vocabulary, which the products read, are zero.
+template <int VS, int TN>
+__device__ __forceinline__ void tile_dz(const VocabArgs& p, const Acc<VS, TN>& acc, const float* s_ref, const float* s_coef,
+                                        const int* s_col, uint8_t* lds, int64_t row_lo, int64_t row_hi, int64_t n, int w,
+                                        int lane) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  typedef __attribute__((address_space(3))) s16x4* lds4;
+  const int c16 = lane & 15, q16 = lane >> 4, wr = w >> 1, wc = w & 1;
+  const float f = p.scale * LOG2E;
+  const int64_t col0 = n * (64 * TN) + 32 * TN * wc;
+  const int left = (int)min((int64_t)(64 * TN), p.width - col0) - c16;  // this lane's column of b exists: 16 b < left
+  uint8_t* t = lds + w * (TN * 1024);
+#pragma unroll
+  for (int a = 0; a < 2 * VS; ++a) {
+    const int row0 = 32 * (2 * (a / 2) + wr) + 16 * (a % 2);
+    const f32x4 ref = *reinterpret_cast<const f32x4*>(s_ref + row0 + 4 * q16);
+    const f32x4 coef = *reinterpret_cast<const f32x4*>(s_coef + row0 + 4 * q16);
+    const i32x4 col = *reinterpret_cast<const i32x4*>(s_col + row0 + 4 * q16);
+    f32x4 v[2 * TN];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+      for (int b = 0; b < 2 * TN; ++b)
+        v[b][r] = coef[r] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[a][b][r], f, -ref[r]));
+      const int hit = col[r] - 32 * TN * wc - c16;  // 16 b: the target is this lane's column b
+      if (__ballot(col[r] >= 0 && hit >= 0 && hit < 32 * TN && hit % 16 == 0)) {
+#pragma unroll
+        for (int b = 0; b < 2 * TN; ++b)
+          if (col[r] >= 0 && hit == 16 * b) v[b][r] -= coef[r];
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2 * TN; ++b) {
+      u32x2 o = {pack_bf16(v[b][0], v[b][1]), pack_bf16(v[b][2], v[b][3])};
+      if (!(16 * b < left)) o = (u32x2){0, 0};
+      *reinterpret_cast<u32x2*>(t + (16 * b + c16) * 32 + q16 * 8) = o;
+    }
+    wave_lds_sync();
+#pragma unroll
+    for (int u = 0; u < TN; ++u) {
+      const int c8 = 8 * (4 * u + q16);  // this lane's columns of row row0 + c16
+      uint8_t* at = t + (c8 + (c16 >> 2)) * 32 + (c16 & 3) * 8;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)at);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 4 * 32));
+      const s16x8 o = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      const int64_t row = row_lo + row0 + c16, c = col0 + c8;
+      if (row < row_hi && c < p.ld) *reinterpret_cast<s16x8*>(p.dz + row * p.ld + c) = o;
+    }
+    wave_lds_sync();
+  }
+}
+
+// Store of a tile, 16 rows of a wave at a time through LDS (2 TN KiB a wave,
+// columns XOR-swizzled by row so that the four lane groups write other banks):
+// 16 bytes a lane, fp32 or bf16, with `add` (may be y itself) added.  row_of: the
+// output row of a row of the tile, -1: none; N columns a row.
+template <int VS, int TN, bool BF, class Row>
+__device__ __forceinline__ void store_tile(const Acc<VS, TN>& acc, uint8_t* lds, void* y, const void* add, int64_t N,
+                                           int64_t col0, int w, int lane, Row&& row_of) {
+  constexpr int CPP = BF ? 8 : 4, LPR = 32 * TN / CPP, U = 16 * LPR / 64, ES = BF ? 2 : 4;
+  const int c16 = lane & 15, q16 = lane >> 4, wr = w >> 1;
+  float* t = reinterpret_cast<float*>(lds + w * (2048 * TN));
+  const int64_t col = col0 + CPP * (lane % LPR);
+#pragma unroll
+  for (int a = 0; a < 2 * VS; ++a) {
+    int64_t at[U];
+    u32x4 av[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = row_of(32 * (2 * (a / 2) + wr) + 16 * (a % 2) + u * (64 / LPR) + lane / LPR);
+      at[u] = row >= 0 && col < N ? (row * N + col) * ES : -1;
+      // all addends of these rows before their first store: add may be y itself
+      if (add && at[u] >= 0) av[u] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(add) + at[u]);
+    }
+#pragma unroll
+    for (int b = 0; b < 2 * TN; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) t[(4 * q16 + r) * (32 * TN) + ((16 * b + c16) ^ (16 * q16))] = acc[a][b][r];
+    wave_lds_sync();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = u * (64 / LPR) + lane / LPR;
+      const f32x4* q = reinterpret_cast<const f32x4*>(t + r * (32 * TN) + ((CPP * (lane % LPR)) ^ (16 * (r >> 2))));
+      u32x4 o;
+      if (BF) {
+        f32x4 x = q[0], z = q[1];
+        if (add) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            x[2 * c] += __uint_as_float(av[u][c] << 16);
+            x[2 * c + 1] += __uint_as_float(av[u][c] & 0xFFFF0000u);
+            z[2 * c] += __uint_as_float(av[u][2 + c] << 16);
+            z[2 * c + 1] += __uint_as_float(av[u][2 + c] & 0xFFFF0000u);
+          }
+        }
+        o = (u32x4){pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+      } else {
+        f32x4 x = q[0];
+        if (add) x += __builtin_bit_cast(f32x4, av[u]);
+        o = __builtin_bit_cast(u32x4, x);
+      }
+      if (at[u] >= 0) __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(static_cast<uint8_t*>(y) + at[u]));
+    }
+    wave_lds_sync();
+  }
+}
+
+// ------------------------------------------------------------------ tiles --
+
+// Row operand: DMA offsets of T slabs of `rows` rows of `rowb` bytes.
 template <int T, int BK>
-__device__ __forceinline__ void rows_operand(BgOperand<T>& o, const int32_t* index, int64_t index_rows, int64_t row0,
-                                             int64_t rows, uint32_t rowb, int w, int lane) {
+__device__ __forceinline__ void rows_operand(BgOperand<T>& o, int64_t rows, uint32_t rowb, int w, int lane) {
   constexpr int CPR = BK / 8;
   const int swz = 16 * ((lane % CPR) ^ bg_row_swz<BK>(64 / CPR * w + lane / CPR));
 #pragma unroll
   for (int i = 0; i < T * BK / 32; ++i) {
-    const int64_t row = row0 + 64 / CPR * (4 * i + w) + lane / CPR;
-    int64_t src = gathered_row(index, index_rows, row, rows);
-    if (!index && src >= 0) src -= row0;
-    o.voff[i] = src >= 0 ? (uint32_t)src * rowb + swz : BG_OOB;
+    const int row = 64 / CPR * (4 * i + w) + lane / CPR;
+    o.voff[i] = row < rows ? (uint32_t)row * rowb + swz : BG_OOB;
   }
 }
-// Column operand: DMA offsets of T slabs of columns [col0, cols), summed rows
-// `stride` bytes apart (gathered: only the column's part).
+// Column operand: DMA offsets of T slabs of `cols` columns, summed rows o.stride
+// bytes apart.
 template <int T, int BK>
-__device__ __forceinline__ void cols_operand(BgOperand<T>& o, bool gathered, int64_t col0, int64_t cols, int w, int lane) {
+__device__ __forceinline__ void cols_operand(BgOperand<T>& o, int64_t cols, int w, int lane) {
 #pragma unroll
   for (int i = 0; i < T * BK / 32; ++i) {
     const int row = (4 * i + w) * (8 / T) + lane / (8 * T);
-    const int c = 8 * ((lane % (8 * T)) ^ bg_col_swz<T>(row));
-    const uint32_t at = gathered ? (uint32_t)(col0 * 2) : (uint32_t)(row * o.stride);
-    o.voff[i] = col0 + c < cols ? at + 2 * c : BG_OOB;
+    const int c = 8 * ((lane % (8 * T)) ^ bg_col_swz16<T>(row));
+    o.voff[i] = c < cols ? (uint32_t)(row * o.stride) + 2 * c : BG_OOB;
   }
 }
 
-// sum over the 32 lanes of each half of a wave (every lane gets it)
-__device__ __forceinline__ float half_sum(float v) {
-  v += __uint_as_float(dpp_mov<0xB1>(__float_as_uint(v)));   // quad_perm [1,0,3,2]
-  v += __uint_as_float(dpp_mov<0x4E>(__float_as_uint(v)));   // quad_perm [2,3,0,1]
-  v += __uint_as_float(dpp_mov<0x141>(__float_as_uint(v)));  // row_half_mirror
-  v += __uint_as_float(dpp_mov<0x140>(__float_as_uint(v)));  // row_mirror
-  return v + __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F));
-}
-
-struct TileParams {  // what bg_sum reads of its arguments
-  const int32_t* row_index;
-  int64_t a_rows;
+struct NoGather {  // bg_sum's arguments: no row of these operands is gathered
+  static constexpr const int32_t* row_index = nullptr;
+  static constexpr int64_t a_rows = 0;
 };
 
-// The sums of a tile's valid slabs, then epi(acc) for VS of them.
-template <int MODE, int TM, int TN, int BK, int KG, class Epi>
-__device__ __forceinline__ void tile_sums(const TileParams& a, const BgTile& tl, BgOperand<TM>& oa, BgOperand<TN>& ob,
-                                          uint8_t* lds, int vs, int nst, int grp, int w, int lane, Epi&& epi) {
+// The sums of a tile's valid slabs, then epi(VS, acc).
+template <int MODE, int TM, int TN, int BK, class Epi>
+__device__ __forceinline__ void tile_sums(const BgTile& tl, BgOperand<TM>& oa, BgOperand<TN>& ob, uint8_t* lds, int vs,
+                                          int w, int lane, Epi&& epi) {
   auto run = [&](auto n) {
     constexpr int VS = decltype(n)::value;
-    f32x16 acc[VS][TN];
-    if (bg_sum<MODE, TM, TN, BK, KG, VS>(a, tl, oa, ob, lds, nst, grp, w, lane, acc)) epi(acc);
+    Acc<VS, TN> acc;
+    bg_sum<MODE, TM, TN, BK, 1, VS, 16>(NoGather(), tl, oa, ob, lds, (int)((tl.K + BK - 1) / BK), 0, w, lane, acc);
+    epi(n, acc);
   };
   if constexpr (TM == 4) {
     if (vs == 4) run(std::integral_constant<int, 4>());
     else if (vs == 3) run(std::integral_constant<int, 3>());
     else if (vs == 2) run(std::integral_constant<int, 2>());
     else run(std::integral_constant<int, 1>());
+  } else if constexpr (TM == 3) {
+    if (vs == 3) run(std::integral_constant<int, 3>());
+    else if (vs == 2) run(std::integral_constant<int, 2>());
+    else run(std::integral_constant<int, 1>());
   } else if constexpr (TM == 2) {
     if (vs == 2) run(std::integral_constant<int, 2>());
     else run(std::integral_constant<int, 1>());
   } else {
-    run(std::integral_constant<int, TM>());
+    run(std::integral_constant<int, 1>());
   }
 }
 
-// Logits of a tile: DZ false leaves its partial sums, DZ true writes dz.
-template <int TM, int TN, bool DZ>
+template <int TM, int TN, int BK, bool DZ>
 __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_logits_kernel(VocabArgs p) {
-  constexpr int BM = 64 * TM, BN = 64 * TN, BK = 64;
+  constexpr int BM = 64 * TM, BN = 64 * TN;
   __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds<TM, TN>()];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t count = *p.count;
-  int64_t m, n;
-  if (!vocab_tile((count + BM - 1) / BM, (p.width + BN - 1) / BN, blockIdx.x, m, n)) return;  // block-uniform
-  BgTile tl;
+  const int64_t count = __builtin_amdgcn_readfirstlane(*p.count), tm = (count + BM - 1) / BM, tn = (p.width + BN - 1) / BN;
+  int64_t t, m, n;
+  if (!vocab_turn(tm * tn, t)) return;  // block-uniform
+  vocab_tile(tm, tn, t, m, n);
+  BgTile tl = {};
   BgOperand<TM> oa;
   BgOperand<TN> ob;
   tl.row_lo = m * BM;
   tl.row_hi = min(count, tl.row_lo + BM);
-  tl.n0 = n * BN;
-  tl.m0 = tl.g = 0;
   tl.K = p.k;
   const uint32_t rowb = (uint32_t)p.k * 2;
-  oa.rsrc = bg_rsrc(p.h, p.rows * (int64_t)rowb);
-  rows_operand<TM, BK>(oa, p.row_index, p.rows, tl.row_lo, tl.row_hi, rowb, w, lane);
-  const int64_t cols = min((int64_t)BN, p.width - tl.n0);
-  ob.rsrc = bg_rsrc(p.w + (p.v0 + tl.n0) * p.k, cols * rowb);
-  rows_operand<TN, BK>(ob, nullptr, cols, 0, cols, rowb, w, lane);
-  const int li = lane & 31, half = lane >> 5, wr = w >> 1, wc = w & 1;
-  const int vs = (int)((tl.row_hi - tl.row_lo + 63) / 64), nst = (int)((p.k + BK - 1) / BK);
-  const TileParams a = {p.row_index, p.rows};
-  tile_sums<BG_FORWARD, TM, TN, BK, 1>(a, tl, oa, ob, lds, vs, nst, 0, w, lane, [&](auto& acc) {
-    constexpr int VS = sizeof(acc) / sizeof(acc[0]);
-    // the tile's rows: reference, and for dz coefficient and target column
+  const int64_t rows = tl.row_hi - tl.row_lo, cols = min((int64_t)BN, p.width - n * BN);
+  oa.rsrc = bg_rsrc(p.hc + tl.row_lo * p.k, rows * rowb);
+  rows_operand<TM, BK>(oa, rows, rowb, w, lane);
+  ob.rsrc = bg_rsrc(p.w + (p.v0 + n * BN) * p.k, cols * rowb);
+  rows_operand<TN, BK>(ob, cols, rowb, w, lane);
+  const RowTerms mine = row_terms<DZ>(p, tl.row_lo + threadIdx.x, tl.row_hi, n * BN, BN);
+  tile_sums<BG_FORWARD, TM, TN, BK>(tl, oa, ob, lds, (int)((rows + 63) / 64), w, lane, [&](auto vs, auto& acc) {
+    constexpr int VS = decltype(vs)::value;
     float* s_ref = reinterpret_cast<float*>(lds);
     float* s_coef = s_ref + BM;
     int* s_col = reinterpret_cast<int*>(s_coef + BM);
-    for (int r = threadIdx.x; r < 64 * VS; r += 256) {
-      const int64_t row = tl.row_lo + r;
-      const bool in = row < tl.row_hi;
+    if (threadIdx.x < BM) {
+      s_ref[threadIdx.x] = mine.ref;
       if (DZ) {
-        s_ref[r] = in ? p.ref[row] : 0.0f;
-        s_coef[r] = in ? p.coef[row] : 0.0f;
-        const int64_t c = in ? (int64_t)p.target[row] - p.v0 - tl.n0 : -1;
-        s_col[r] = c >= 0 && c < BN ? (int)c : -1;
-      } else {
-        s_ref[r] = in ? p.ref[p.row_index[row]] : 0.0f;
+        s_coef[threadIdx.x] = mine.coef;
+        s_col[threadIdx.x] = mine.col;
       }
     }
     __syncthreads();
-    const float f = p.scale * LOG2E;
-    const int64_t left = p.width - tl.n0 - 32 * TN * wc - li;  // this lane's column of j exists: 32 j < left
-    if constexpr (!DZ) {
-      // partial sums of this wave's columns; the two column halves meet in LDS
-      float2* s_part = reinterpret_cast<float2*>(lds + 16 * 1024);
-#pragma unroll
-      for (int i = 0; i < VS; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row0 = 32 * (2 * i + wr) + 8 * q + 4 * half;
-          const f32x4 ref = *reinterpret_cast<const f32x4*>(s_ref + row0);
-          float s[4], top[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            s[r] = 0.0f;
-            top[r] = ref[r];
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-              s[r] += 32 * j < left ? __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][4 * q + r], f, -ref[r])) : 0.0f;
-          }
-          bool over = false;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            s[r] = half_sum(s[r]);
-            over |= !(s[r] < 0x1p120f);
-          }
-          if (__ballot(over)) {  // wave-uniform: relative to the row's maximum here
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float t = -__builtin_inff();
-#pragma unroll
-              for (int j = 0; j < TN; ++j)
-                t = 32 * j < left ? __builtin_fmaxf(t, acc[i][j][4 * q + r] * f) : t;
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) t = __builtin_fmaxf(t, __shfl_xor(t, o, 64));
-              float u = 0.0f;
-#pragma unroll
-              for (int j = 0; j < TN; ++j)
-                u += 32 * j < left && !(acc[i][j][4 * q + r] * f == -__builtin_inff())
-                         ? __builtin_amdgcn_exp2f(acc[i][j][4 * q + r] * f - t) : 0.0f;
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) u += __shfl_xor(u, o, 64);
-              // of this row alone: its neighbours keep their bits
-              if (!(s[r] < 0x1p120f)) {
-                s[r] = u;
-                top[r] = t;
-              }
-            }
-          }
-          if (li == 0) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s_part[wc * BM + row0 + r] = make_float2(top[r], s[r]);
-          }
-        }
-      __syncthreads();
-      for (int r = threadIdx.x; r < 64 * VS; r += 256) {
-        if (tl.row_lo + r >= tl.row_hi) continue;
-        const float2 a0 = s_part[r], a1 = s_part[BM + r];
-        float2 o = make_float2(__builtin_fmaxf(a0.x, a1.x), 0.0f);
-        if (a0.x == a1.x) o.y = a0.y + a1.y;
-        else o.y = a0.y * __builtin_amdgcn_exp2f(a0.x - o.x) + a1.y * __builtin_amdgcn_exp2f(a1.x - o.x);
-        p.part[n * p.rows + tl.row_lo + r] = o;
-      }
-    } else {
-      // dz, 32 rows of this wave at a time through LDS: 16 bytes a lane and
-      // whole row segments per store.  Columns past the vocabulary, which the
-      // products read, are zero.
-      constexpr int RS = 64 * TN + 16;  // bytes of an LDS row
-      uint8_t* t = lds + 16 * 1024 + w * 32 * RS;
-      const int64_t col0 = tl.n0 + 32 * TN * wc;
-#pragma unroll
-      for (int i = 0; i < VS; ++i) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row0 = 32 * (2 * i + wr) + 8 * q + 4 * half;
-          const f32x4 ref = *reinterpret_cast<const f32x4*>(s_ref + row0);
-          const f32x4 coef = *reinterpret_cast<const f32x4*>(s_coef + row0);
-          typedef int i32x4v __attribute__((ext_vector_type(4)));
-          const i32x4v col = *reinterpret_cast<const i32x4v*>(s_col + row0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-              const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][4 * q + r], f, -ref[r]));
-              const float one = col[r] == 32 * (TN * wc + j) + li ? 1.0f : 0.0f;
-              const float v = 32 * j < left ? coef[r] * (pr - one) : 0.0f;
-              *reinterpret_cast<uint16_t*>(t + (8 * q + 4 * half + r) * RS + (32 * j + li) * 2) = to_bf16(v);
-            }
-        }
-        wave_lds_sync();
-        constexpr int LPR = 4 * TN, U = 32 * LPR / 64;  // lanes a row, stores a slab
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int r = u * (64 / LPR) + lane / LPR;
-          const int64_t row = tl.row_lo + 32 * (2 * i + wr) + r, c = col0 + 8 * (lane % LPR);
-          if (row < tl.row_hi && c < p.ld)
-            *reinterpret_cast<u32x4*>(p.dz + row * p.ld + c) =
-                *reinterpret_cast<const u32x4*>(t + r * RS + (lane % LPR) * 16);
-        }
-        wave_lds_sync();
-      }
-    }
+    if constexpr (DZ) tile_dz<VS, TN>(p, acc, s_ref, s_coef, s_col, lds + 4096, tl.row_lo, tl.row_hi, n, w, lane);
+    else tile_part<VS, TM, TN>(p, acc, s_ref, reinterpret_cast<float2*>(lds + 4096), tl.row_lo, tl.row_hi, n, w, lane);
   });
 }
 
-// Store of a tile through LDS, slab by slab: rows of `rows` that exist from
-// out_row on, columns of N, fp32 or bf16, with `add` (may be y itself) added.
-template <int VS, int TN, bool BF, class Row>
-__device__ __forceinline__ void store_tile(const f32x16 (&acc)[VS][TN], uint8_t* lds, void* y, const void* add, int64_t N,
-                                           int64_t col0, int w, int lane, Row&& row_at_slab) {
-  constexpr int RS = 128 * TN + 32, CPP = BF ? 8 : 4, LPR = 32 * TN / CPP, U = 32 * LPR / 64, ES = BF ? 2 : 4;
-  const int li = lane & 31, half = lane >> 5, wr = w >> 1;
-  float* t = reinterpret_cast<float*>(lds + w * 32 * RS);
-  const int64_t col = col0 + CPP * (lane % LPR);
-#pragma unroll
-  for (int i = 0; i < VS; ++i) {
-    int64_t at[U];
-    u32x4 av[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = row_at_slab(32 * (2 * i + wr) + u * (64 / LPR) + lane / LPR);
-      at[u] = row >= 0 && col < N ? (row * N + col) * ES : -1;
-      // all of the slab's addends before its first store: add may be y itself
-      if (add && at[u] >= 0) av[u] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(add) + at[u]);
-    }
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) t[((8 * (r >> 2) + 4 * half + (r & 3)) * RS + (32 * j + li) * 4) / 4] = acc[i][j][r];
-    wave_lds_sync();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = u * (64 / LPR) + lane / LPR;
-      const f32x4* q = reinterpret_cast<const f32x4*>(reinterpret_cast<const uint8_t*>(t) + r * RS + (lane % LPR) * 4 * CPP);
-      u32x4 o;
-      if (BF) {
-        f32x4 a = q[0], b = q[1];
-        if (add) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            a[2 * c] += __uint_as_float(av[u][c] << 16);
-            a[2 * c + 1] += __uint_as_float(av[u][c] & 0xFFFF0000u);
-            b[2 * c] += __uint_as_float(av[u][2 + c] << 16);
-            b[2 * c + 1] += __uint_as_float(av[u][2 + c] & 0xFFFF0000u);
-          }
-        }
-        o = (u32x4){pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
-      } else {
-        f32x4 a = q[0];
-        if (add) a += __builtin_bit_cast(f32x4, av[u]);
-        o = __builtin_bit_cast(u32x4, a);
-      }
-      if (at[u] >= 0)
-        __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(static_cast<uint8_t*>(y) + at[u]));
-    }
-    wave_lds_sync();
-  }
-}
-
-// sums[split] += dz w over the split's part of the piece (= in the first piece)
 template <int TM, int TN, int BK>
 __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_dh_kernel(VocabArgs p) {
   constexpr int BM = 64 * TM, BN = 64 * TN;
   __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds<TM, TN>()];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t count = *p.count;
-  // a split's tiles follow one another; a row's splits lie along m
-  const int64_t tm = (count + BM - 1) / BM, tn = (p.k + BN - 1) / BN;
-  int64_t m, n;
-  if (!vocab_tile(tm * p.splits, tn, blockIdx.x, m, n)) return;  // block-uniform
-  const int64_t split = m / tm, s0 = split * p.per_split;
-  BgTile tl;
+  const int64_t count = __builtin_amdgcn_readfirstlane(*p.count), tm = (count + BM - 1) / BM, tn = (p.k + BN - 1) / BN;
+  int64_t t, m, n;
+  if (!vocab_turn(tm * p.splits * tn, t)) return;  // block-uniform
+  vocab_tile(tm * p.splits, tn, t, m, n);
+  const int64_t split = __builtin_amdgcn_readfirstlane((uint32_t)m / (uint32_t)tm), s0 = split * p.per_split;
+  BgTile tl = {};
   BgOperand<TM> oa;
   BgOperand<TN> ob;
-  tl.row_lo = (m % tm) * BM;
+  tl.row_lo = (m - split * tm) * BM;
   tl.row_hi = min(count, tl.row_lo + BM);
-  tl.n0 = n * BN;
-  tl.m0 = tl.g = 0;
   tl.K = max((int64_t)0, min(p.per_split, p.width - s0));
-  const uint32_t rowb = (uint32_t)p.ld * 2;
+  const int64_t rows = tl.row_hi - tl.row_lo;
   // a split past a short last piece has nothing to sum: no byte of dz either
-  oa.rsrc = bg_rsrc(p.dz + tl.row_lo * p.ld + s0, tl.K > 0 ? (tl.row_hi - tl.row_lo) * (int64_t)rowb - s0 * 2 : 0);
-  rows_operand<TM, BK>(oa, nullptr, count, tl.row_lo, tl.row_hi, rowb, w, lane);
+  oa.rsrc = bg_rsrc(p.dz + tl.row_lo * p.ld + s0, tl.K > 0 ? rows * p.ld * 2 - s0 * 2 : 0);
+  rows_operand<TM, BK>(oa, rows, (uint32_t)p.ld * 2, w, lane);
   ob.stride = p.k * 2;
-  ob.base = reinterpret_cast<const uint8_t*>(p.w + (p.v0 + s0) * p.k + tl.n0);
-  cols_operand<TN, BK>(ob, false, tl.n0, p.k, w, lane);
-  const int vs = (int)((tl.row_hi - tl.row_lo + 63) / 64), nst = (int)((tl.K + BK - 1) / BK);
-  const TileParams a = {nullptr, count};
-  tile_sums<BG_DGRAD, TM, TN, BK, 1>(a, tl, oa, ob, lds, vs, nst, 0, w, lane, [&](auto& acc) {
-    constexpr int VS = sizeof(acc) / sizeof(acc[0]);
+  ob.base = reinterpret_cast<const uint8_t*>(p.w + (p.v0 + s0) * p.k + n * BN);
+  cols_operand<TN, BK>(ob, p.k - n * BN, w, lane);
+  tile_sums<BG_DGRAD, TM, TN, BK>(tl, oa, ob, lds, (int)((rows + 63) / 64), w, lane, [&](auto vs, auto& acc) {
     float* y = p.sums + split * p.rows * p.k;
-    store_tile<VS, TN, false>(acc, lds, y, p.first ? nullptr : y, p.k, tl.n0 + 32 * TN * (w & 1), w, lane, [&](int r) {
-      return tl.row_lo + r < tl.row_hi ? tl.row_lo + r : (int64_t)-1;
-    });
+    store_tile<decltype(vs)::value, TN, false>(acc, lds, y, p.first ? nullptr : y, p.k, n * BN + 32 * TN * (w & 1), w, lane,
+        [&](int r) { return tl.row_lo + r < tl.row_hi ? tl.row_lo + r : (int64_t)-1; });
   });
 }
 
-// dw of the piece's rows of w = add + dz^T h
 template <int TM, int TN, int BK>
 __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_dw_kernel(VocabArgs p) {
   constexpr int BM = 64 * TM, BN = 64 * TN;
   __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds<TM, TN>()];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t count = *p.count;
-  int64_t m, n;
-  if (!vocab_tile((p.width + BM - 1) / BM, (p.k + BN - 1) / BN, blockIdx.x, m, n)) return;  // block-uniform
-  BgTile tl;
+  const int64_t count = __builtin_amdgcn_readfirstlane(*p.count), tm = (p.width + BM - 1) / BM, tn = (p.k + BN - 1) / BN;
+  int64_t t, m, n;
+  if (!vocab_turn(tm * tn, t)) return;  // block-uniform
+  vocab_tile(tm, tn, t, m, n);
+  BgTile tl = {};
   BgOperand<TM> oa;
   BgOperand<TN> ob;
-  tl.row_lo = 0;
-  tl.row_hi = tl.K = count;
-  tl.m0 = m * BM;
-  tl.n0 = n * BN;
-  tl.g = 0;
+  tl.row_lo = m * BM;
+  tl.row_hi = min(p.width, tl.row_lo + BM);
+  tl.K = count;
   oa.stride = p.ld * 2;
-  oa.base = reinterpret_cast<const uint8_t*>(p.dz + tl.m0);
-  cols_operand<TM, BK>(oa, false, tl.m0, p.ld, w, lane);
+  oa.base = reinterpret_cast<const uint8_t*>(p.dz + tl.row_lo);
+  cols_operand<TM, BK>(oa, p.ld - tl.row_lo, w, lane);
   ob.stride = p.k * 2;
-  ob.rsrc = bg_rsrc(p.h, p.rows * p.k * 2);
-  cols_operand<TN, BK>(ob, true, tl.n0, p.k, w, lane);
-  const int vs = (int)min((int64_t)TM, (p.width - tl.m0 + 63) / 64), nst = (int)((count + BK - 1) / BK);
-  const TileParams a = {p.row_index, p.rows};
-  tile_sums<BG_WGRAD, TM, TN, BK, 1>(a, tl, oa, ob, lds, vs, nst, 0, w, lane, [&](auto& acc) {
-    constexpr int VS = sizeof(acc) / sizeof(acc[0]);
-    auto row = [&](int r) { return tl.m0 + r < p.width ? p.v0 + tl.m0 + r : (int64_t)-1; };
-    const int64_t col0 = tl.n0 + 32 * TN * (w & 1);
+  ob.base = reinterpret_cast<const uint8_t*>(p.hc + n * BN);
+  cols_operand<TN, BK>(ob, p.k - n * BN, w, lane);
+  tile_sums<BG_WGRAD, TM, TN, BK>(tl, oa, ob, lds, (int)((tl.row_hi - tl.row_lo + 63) / 64), w, lane, [&](auto vs, auto& acc) {
+    constexpr int VS = decltype(vs)::value;
+    auto row = [&](int r) { return tl.row_lo + r < tl.row_hi ? p.v0 + tl.row_lo + r : (int64_t)-1; };
+    const int64_t col0 = n * BN + 32 * TN * (w & 1);
     if (p.dw_bf) store_tile<VS, TN, true>(acc, lds, p.dw, p.add, p.k, col0, w, lane, row);
     else store_tile<VS, TN, false>(acc, lds, p.dw, p.add, p.k, col0, w, lane, row);
   });
@@ -478,11 +568,13 @@ __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_dw_kernel(Vo
 
 // ------------------------------------------------------------------- ends --
 
-constexpr int JOIN_ROWS = 16;  // rows of a block, 64 threads each
+// R rows of a block, 1024 / R threads each, which take every 1024 / R-th tile.
+template <int R>
 __global__ __launch_bounds__(1024) void vocab_join_kernel(VocabArgs p, int64_t tiles) {
-  __shared__ float2 s_part[64][JOIN_ROWS];
-  const int r = threadIdx.x % JOIN_ROWS, sl = threadIdx.x / JOIN_ROWS;
-  const int64_t count = *p.count, row = (int64_t)blockIdx.x * JOIN_ROWS + r;
+  constexpr int S = 1024 / R, AHEAD = 8;
+  __shared__ float2 s_part[S][R];
+  const int r = threadIdx.x % R, sl = threadIdx.x / R;
+  const int64_t count = *p.count, row = (int64_t)blockIdx.x * R + r;
   // rows without a target, by their own index
   if (sl == 0 && row < p.rows && !has_target(p, row)) p.loss[row] = p.lse[row] = 0.0f;
   auto add = [](float2& a, float2 b) {
@@ -495,14 +587,23 @@ __global__ __launch_bounds__(1024) void vocab_join_kernel(VocabArgs p, int64_t t
     }
   };
   float2 sum = make_float2(0.0f, 0.0f);
+  float ref = 0.0f;
+  int32_t at = 0;
   if (row < count) {
-    sum.x = p.ref[p.row_index[row]];
-#pragma unroll 4
-    for (int64_t t = sl; t < tiles; t += 64) add(sum, p.part[t * p.rows + row]);
+    at = p.row_index[row];
+    sum.x = ref = p.ref[row];
+    for (int64_t t = sl; t < tiles; t += AHEAD * S) {
+      float2 v[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) v[k] = p.part[min(t + k * S, tiles - 1) * p.rows + row];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (t + k * S < tiles) add(sum, v[k]);
+    }
   }
   s_part[sl][r] = sum;
   __syncthreads();
-  for (int o = 32; o >= 1; o >>= 1) {
+  for (int o = S / 2; o >= 1; o >>= 1) {
     if (sl < o) {
       add(sum, s_part[sl + o][r]);
       s_part[sl][r] = sum;
@@ -510,28 +611,51 @@ __global__ __launch_bounds__(1024) void vocab_join_kernel(VocabArgs p, int64_t t
     __syncthreads();
   }
   if (sl == 0 && row < count) {
-    const int32_t at = p.row_index[row];
-    const float ref = p.ref[at], l = __builtin_log2f(sum.y);
+    const float l = __builtin_log2f(sum.y);
     p.lse[at] = (sum.x + l) * LN2;
     p.loss[at] = ((sum.x - ref) + l) * LN2;
   }
 }
 
-// dh of every row: its splits' sums added in order, zeros without a target
+// dh of every row: its splits' sums, zeros without a target.  Thread 32 g + i of a
+// block takes splits g, g + 8, .. of 8 columns, and the eight are added in order.
 __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabArgs p) {
-  const int64_t slots = p.k / 8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.rows * slots; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / slots, e = 8 * (i % slots);
-    const int32_t at = p.number[row];
+  __shared__ f32x4 s_sum[8][32][2];
+  const int g = threadIdx.x >> 5, i = threadIdx.x & 31;
+  const int64_t slots = p.k / 8, items = p.rows * slots;
+  for (int64_t i0 = (int64_t)blockIdx.x * 32; i0 < items; i0 += (int64_t)gridDim.x * 32) {
+    const int64_t item = i0 + i, row = item / slots, e = 8 * (item % slots);
+    const int32_t at = item < items ? p.number[row] : -1;
     f32x4 a = {0, 0, 0, 0}, b = a;
     if (at >= 0)
-      for (int s = 0; s < p.splits; ++s) {
-        const f32x4* q = reinterpret_cast<const f32x4*>(p.sums + ((int64_t)s * p.rows + at) * p.k + e);
-        a += q[0];
-        b += q[1];
+      for (int s0 = g; s0 < p.splits; s0 += 32) {  // four in flight
+        f32x4 u[4], v[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const f32x4* q = reinterpret_cast<const f32x4*>(p.sums + ((int64_t)min(s0 + 8 * s, p.splits - 1) * p.rows + at) * p.k + e);
+          u[s] = __builtin_nontemporal_load(q);
+          v[s] = __builtin_nontemporal_load(q + 1);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          if (s0 + 8 * s < p.splits) {
+            a += u[s];
+            b += v[s];
+          }
       }
-    const u32x4 o = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
-    __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p.dh + row * p.k + e));
+    s_sum[g][i][0] = a;
+    s_sum[g][i][1] = b;
+    __syncthreads();
+    if (g == 0 && item < items) {
+#pragma unroll
+      for (int o = 1; o < 8; ++o) {
+        a += s_sum[o][i][0];
+        b += s_sum[o][i][1];
+      }
+      const u32x4 o = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
+      __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p.dh + row * p.k + e));
+    }
+    __syncthreads();
   }
 }
 
@@ -541,53 +665,98 @@ static int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 static int64_t tiles_of(int64_t rows, int64_t cols, int TM, int TN) {
   return ((rows + 64 * TM - 1) / (64 * TM)) * ((cols + 64 * TN - 1) / (64 * TN));
 }
+// blocks for `tiles` tiles of one block each: every XCD's share rounded up
 static dim3 tile_grid(int64_t tiles) { return dim3((unsigned)(8 * (tiles / 8 + 1))); }
 
-// Columns (in 64s) of a tile of the logits.
-static int logits_tn(int64_t rows) { return rows > 128 ? 4 : 2; }
-static int64_t forward_tiles(int64_t rows, int64_t vocab) { return (vocab + 64 * logits_tn(rows) - 1) / (64 * logits_tn(rows)); }
-
+// Tile of the logits (64 TM rows by 64 TN columns; measured with k = 1032 or
+// 2048, the dz form).  The large tile reads its operands least, and from two
+// rounds of tiles on it is the fastest (8192 rows, vocabulary 131072: see
+// above; 1000 rows: 461 us, 192 x 128 678, 128 x 128 574); where its second row
+// of tiles would be mostly empty, or with few tiles, smaller ones (300 rows:
+// 192 x 128 202 us, 256 x 256 219; 64 rows, vocabulary 32003: 64 x 128 16 us,
+// 256 x 256 19).
+struct TileShape {
+  int tm, tn;
+};
+static TileShape logits_shape(int64_t rows, int64_t cols) {
+  if (rows > 384 && tiles_of(rows, cols, 4, 4) >= 256) return {4, 4};
+  if (rows > 64 && tiles_of(rows, cols, 3, 2) >= 256) return {3, 2};
+  return {1, 2};
+}
+static int64_t forward_tiles(int64_t rows, int64_t vocab) {
+  const int bn = 64 * logits_shape(rows, vocab).tn;
+  return (vocab + bn - 1) / bn;
+}
 template <bool DZ>
 static void launch_logits(const VocabArgs& p, hipStream_t str) {
-  if (p.rows > 128)
-    hipLaunchKernelGGL((vocab_logits_kernel<4, 4, DZ>), tile_grid(tiles_of(p.rows, p.width, 4, 4)), dim3(256), 0, str, p);
-  else if (p.rows > 64)
-    hipLaunchKernelGGL((vocab_logits_kernel<2, 2, DZ>), tile_grid(tiles_of(p.rows, p.width, 2, 2)), dim3(256), 0, str, p);
-  else
-    hipLaunchKernelGGL((vocab_logits_kernel<1, 2, DZ>), tile_grid(tiles_of(p.rows, p.width, 1, 2)), dim3(256), 0, str, p);
+  const TileShape t = logits_shape(p.rows, p.width);
+  const dim3 grid = tile_grid(tiles_of(p.rows, p.width, t.tm, t.tn));
+  if (t.tm == 4) hipLaunchKernelGGL((vocab_logits_kernel<4, 4, 64, DZ>), grid, dim3(256), 0, str, p);
+  else if (t.tm == 3) hipLaunchKernelGGL((vocab_logits_kernel<3, 2, 32, DZ>), grid, dim3(256), 0, str, p);
+  else hipLaunchKernelGGL((vocab_logits_kernel<1, 2, 64, DZ>), grid, dim3(256), 0, str, p);
 }
 
-// The pieces of the vocabulary in the backward pass and the splits of dh.
+// The pieces of the vocabulary in the backward pass, and tile and splits of dh.
 struct VocabPlan {
-  int64_t width, ld, pieces, splits, per_split;
+  int64_t width, ld, splits, per_split;
+  TileShape dh, dw;
 };
 static VocabPlan vocab_plan(int64_t rows, int64_t vocab, int64_t k) {
   VocabPlan q;
-  // dz of a piece stays below 128 MB, so that it is still in the memory-side
-  // cache when the two products read it
-  int64_t most = ((int64_t)1 << 26) / (rows > 0 ? rows : 1);
+  // dz of a piece takes up to 512 MiB: fewer pieces add to dh's sums less often
+  // (8192 rows, vocabulary 131072, k = 2048, 256 x 256 tiles of dh: pieces of
+  // 256 MiB 3609 us, 512 MiB 3448, 1 GiB 3191)
+  int64_t most = ((int64_t)1 << 28) / (rows > 0 ? rows : 1);
   most = most < 2048 ? 2048 : most;
-  q.pieces = (vocab + most - 1) / most;
-  q.pieces = q.pieces < 1 ? 1 : q.pieces;
-  q.width = up((vocab + q.pieces - 1) / q.pieces, 256);
+  const int64_t pieces = vocab > most ? (vocab + most - 1) / most : 1;
+  q.width = up((vocab + pieces - 1) / pieces, 256);
   q.width = q.width < 256 ? 256 : q.width;
-  q.pieces = (vocab + q.width - 1) / q.width;
-  q.pieces = q.pieces < 1 ? 1 : q.pieces;
-  q.ld = q.width;
-  const int64_t tiles = rows > 64 ? tiles_of(rows, k, 2, 4) : tiles_of(rows, k, 1, 2);
-  q.splits = tiles > 0 && tiles < 256 ? (512 + tiles - 1) / tiles : 1;
-  const int64_t room = q.width / 512 > 0 ? q.width / 512 : 1;  // a split sums 512 rows of w at least
-  q.splits = q.splits < room ? q.splits : room;
+  // rows of dz lie 128 bytes off a power of two: its columns would otherwise
+  // fall on few memory channels (writing and reading dz 3 to 6% faster)
+  q.ld = q.width + 64;
+  // dh: the sum over the vocabulary is split over blocks, 512 rows of w each at
+  // least.  256 x 256 tiles run one a CU in whole rounds; a tile's start and
+  // store cost as much as about 1500 rows of w.  Their splits are those of the
+  // shortest rounds, with all, three quarters or half of the rows counted.
+  const int64_t room = q.width / 512 > 0 ? q.width / 512 : 1;
+  int64_t best = 0, splits = 1;
+  for (int64_t s = 1; s <= 32 && s <= room; ++s) {
+    int64_t cost = 0;
+    for (int f = 2; f <= 4; ++f)
+      cost += (tiles_of((rows * f + 3) / 4, k, 4, 4) * s + 255) / 256 * (q.width / s + 1500);
+    if (s == 1 || cost < best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  // They are the fastest where a tile's sum is long (1000 rows, vocabulary
+  // 131072: 508 us, 128 x 256 562); else 128 x 256, two a CU (1000 rows,
+  // vocabulary 32003, k = 1032: 105 us against 143), and 128 x 128 for few rows,
+  // whose sums are split least (301 rows: 38 us against 57).
+  if (rows > 64 && q.width / splits >= 4096) {
+    q.dh = {4, 4};
+  } else {
+    q.dh = rows > 512 ? TileShape{2, 4} : rows > 64 ? TileShape{2, 2} : TileShape{1, 2};
+    const int64_t tiles = tiles_of(rows, k, q.dh.tm, q.dh.tn);
+    splits = tiles > 0 ? (512 + tiles - 1) / tiles : 1;
+    splits = splits < room ? splits : room;
+  }
+  q.splits = splits;
   q.per_split = up((q.width + q.splits - 1) / q.splits, 64);
+  // dw: the sum over the rows is short; two 256 x 128 tiles a CU, one of which
+  // stores while the other multiplies, until it is long (8192 rows: 256 x 256
+  // 2752 us, 256 x 128 2858; 1000 rows, vocabulary 131072: 544 and 502; 64 rows,
+  // vocabulary 32003: 256 x 128 38 us, 128 x 128 34)
+  q.dw = rows > 2048 ? TileShape{4, 4} : rows > 64 ? TileShape{4, 2} : TileShape{2, 2};
   return q;
 }
 
-static int64_t forward_bytes(int64_t rows, int64_t vocab) {
-  return 16 + up(rows, 4) * 4 * 2 + forward_tiles(rows, vocab) * rows * 8;
+static int64_t forward_bytes(int64_t rows, int64_t vocab, int64_t k) {
+  return 16 + up(rows, 4) * 4 * 2 + up(rows * k * 2, 16) + forward_tiles(rows, vocab) * rows * 8;
 }
 static int64_t backward_bytes(int64_t rows, int64_t vocab, int64_t k) {
   const VocabPlan q = vocab_plan(rows, vocab, k);
-  return 16 + up(rows, 4) * 4 * 5 + up(rows * q.ld * 2, 16) + q.splits * rows * k * 4;
+  return 16 + up(rows, 4) * 4 * 5 + up(rows * k * 2, 16) + up(rows * q.ld * 2, 16) + q.splits * rows * k * 4;
 }
 
 }  // namespace nvfp4
@@ -596,14 +765,25 @@ using nvfp4host::aligned;
 
 static int vocab_sizes(int64_t rows, int64_t vocab, int64_t k, float scale) {
   if (rows < 0 || vocab < 0 || k < 0 || !(scale - scale == 0.0f)) return NVFP4_ERROR_INVALID_VALUE;
-  const int64_t lim = (int64_t)1 << 31;
-  if (k % 8 != 0 || k > ((int64_t)1 << 20) || vocab > ((int64_t)1 << 24)) return NVFP4_ERROR_UNSUPPORTED_SHAPE;
-  if (rows >= lim || rows * (k > 0 ? k : 1) * 2 >= lim) return NVFP4_ERROR_UNSUPPORTED_SHAPE;
+  if (k % 8 != 0 || k > ((int64_t)1 << 20) || vocab > ((int64_t)1 << 24) || rows > ((int64_t)1 << 24))
+    return NVFP4_ERROR_UNSUPPORTED_SHAPE;
   return NVFP4_SUCCESS;
 }
 
+// The rows with a target numbered and brought together.
+template <bool FORWARD>
+static void launch_rows(const nvfp4::VocabArgs& p, hipStream_t str) {
+  const int64_t need = (p.rows + 3) / 4, cap = (int64_t)nvfp4host::num_cus() * 8;
+  if (p.rows <= nvfp4::FEW_ROWS) {
+    hipLaunchKernelGGL((nvfp4::vocab_rows_kernel<FORWARD, true>), dim3((unsigned)need), dim3(256), 0, str, p);
+  } else {
+    hipLaunchKernelGGL(nvfp4::vocab_number_kernel, dim3(1), dim3(1024), 0, str, p);
+    hipLaunchKernelGGL((nvfp4::vocab_rows_kernel<FORWARD, false>), dim3((unsigned)(need < cap ? need : cap)), dim3(256), 0, str, p);
+  }
+}
+
 extern "C" int64_t nvfp4_vocab_loss_workspace(int64_t rows, int64_t vocab, int64_t k) {
-  return rows <= 0 || vocab_sizes(rows, vocab, k, 1.0f) ? 0 : nvfp4::forward_bytes(rows, vocab);
+  return rows <= 0 || vocab_sizes(rows, vocab, k, 1.0f) ? 0 : nvfp4::forward_bytes(rows, vocab, k);
 }
 
 extern "C" int nvfp4_vocab_loss(const uint16_t* h, const uint16_t* w, const int32_t* targets, int64_t rows,
@@ -626,14 +806,17 @@ extern "C" int nvfp4_vocab_loss(const uint16_t* h, const uint16_t* w, const int3
   const int64_t list = nvfp4::up(rows, 4);
   p.count = ws;
   p.row_index = ws + 4;
-  p.ref = reinterpret_cast<float*>(ws + 4 + list);
-  p.part = reinterpret_cast<float2*>(ws + 4 + 2 * list);
+  p.ref = reinterpret_cast<float*>(p.row_index + list);
+  p.hc = reinterpret_cast<uint16_t*>(p.ref + list);
+  p.part = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(p.hc) + nvfp4::up(rows * k * 2, 16));
   hipStream_t str = (hipStream_t)stream;
-  const int64_t cap = (int64_t)nvfp4host::num_cus() * 4, dots = (rows + 15) / 16;
-  hipLaunchKernelGGL(nvfp4::vocab_rows_kernel, dim3((unsigned)(1 + (dots < cap ? dots : cap))), dim3(1024), 0, str, p);
+  launch_rows<true>(p, str);  // no row of an empty vocabulary reads w
   if (vocab > 0) nvfp4::launch_logits<false>(p, str);
-  hipLaunchKernelGGL(nvfp4::vocab_join_kernel, dim3((unsigned)((rows + nvfp4::JOIN_ROWS - 1) / nvfp4::JOIN_ROWS)),
-                     dim3(1024), 0, str, p, nvfp4::forward_tiles(rows, vocab));
+  const int64_t tiles = nvfp4::forward_tiles(rows, vocab);
+  if (rows > 1024)  // whole 128-byte lines of a tile's partial sums; with few rows more CUs
+    hipLaunchKernelGGL(nvfp4::vocab_join_kernel<16>, dim3((unsigned)((rows + 15) / 16)), dim3(1024), 0, str, p, tiles);
+  else
+    hipLaunchKernelGGL(nvfp4::vocab_join_kernel<2>, dim3((unsigned)((rows + 1) / 2)), dim3(1024), 0, str, p, tiles);
   return nvfp4host::launch_status();
 }
 
@@ -653,13 +836,13 @@ extern "C" int nvfp4_vocab_loss_backward(const uint16_t* h, const uint16_t* w, c
   if (rows > 0 && (!h || !targets || !lse || !d_loss)) return NVFP4_ERROR_INVALID_VALUE;
   if (vocab > 0 && !w) return NVFP4_ERROR_INVALID_VALUE;
   if (!workspace || workspace_bytes < nvfp4_vocab_loss_backward_workspace(rows, vocab, k)) return NVFP4_ERROR_INVALID_VALUE;
-  if (!nvfp4::tile_grid_ok(rows, 0, vocab) || !nvfp4::tile_grid_ok(vocab, 0, k) || !nvfp4::tile_grid_ok(rows, 0, k))
+  const nvfp4::VocabPlan q = nvfp4::vocab_plan(rows, vocab, k);
+  if (!nvfp4::tile_grid_ok(rows, 0, vocab) || !nvfp4::tile_grid_ok(vocab, 0, k) || !nvfp4::tile_grid_ok(rows * q.splits, 0, k))
     return NVFP4_ERROR_UNSUPPORTED_SHAPE;
   if (!aligned(h, 16) || !aligned(w, 16) || !aligned(targets, 4) || !aligned(lse, 4) || !aligned(d_loss, 4) ||
       !aligned(add, 16) || !aligned(dh, 16) || !aligned(dw, 16) || !aligned(workspace, 16))
     return NVFP4_ERROR_MISALIGNED;
   if ((st = nvfp4host::check_arch())) return st;
-  const nvfp4::VocabPlan q = nvfp4::vocab_plan(rows, vocab, k);
   nvfp4::VocabArgs p{};
   p.h = h; p.w = w; p.targets = targets; p.rows = rows; p.vocab = vocab; p.k = k; p.scale = scale;
   p.lse_in = lse; p.d_loss = d_loss; p.add = add; p.dh = dh; p.dw = dw; p.dw_bf = dw_type == NVFP4_TYPE_BF16;
@@ -671,32 +854,36 @@ extern "C" int nvfp4_vocab_loss_backward(const uint16_t* h, const uint16_t* w, c
   p.target = p.number + list;
   p.ref = reinterpret_cast<float*>(p.target + list);
   p.coef = p.ref + list;
-  p.dz = reinterpret_cast<uint16_t*>(p.coef + list);
+  p.hc = reinterpret_cast<uint16_t*>(p.coef + list);
+  p.dz = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(p.hc) + nvfp4::up(rows * k * 2, 16));
   p.sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.dz) + nvfp4::up(rows * q.ld * 2, 16));
   p.splits = (int)q.splits;
   p.per_split = q.per_split;
+  p.ld = q.ld;
   hipStream_t str = (hipStream_t)stream;
-  hipLaunchKernelGGL(nvfp4::vocab_rows_kernel, dim3(1), dim3(1024), 0, str, p);
+  if (rows > 0) launch_rows<false>(p, str);
+  else hipLaunchKernelGGL(nvfp4::vocab_number_kernel, dim3(1), dim3(1024), 0, str, p);  // none: the count
   for (int64_t v0 = 0; v0 < vocab; v0 += q.width) {
     p.v0 = v0;
     p.width = vocab - v0 < q.width ? vocab - v0 : q.width;
-    p.ld = nvfp4::up(p.width, 8);
     p.first = v0 == 0;
     if (rows > 0) nvfp4::launch_logits<true>(p, str);
     if (dh && rows > 0) {
-      if (rows > 64)
-        hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<2, 4, 32>),
-                           nvfp4::tile_grid(nvfp4::tiles_of(rows, k, 2, 4) * q.splits), dim3(256), 0, str, p);
-      else
-        hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<1, 2, 64>),
-                           nvfp4::tile_grid(nvfp4::tiles_of(rows, k, 1, 2) * q.splits), dim3(256), 0, str, p);
+      const dim3 grid = nvfp4::tile_grid(nvfp4::tiles_of(rows, k, q.dh.tm, q.dh.tn) * q.splits);
+      if (q.dh.tm == 4) hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<4, 4, 64>), grid, dim3(256), 0, str, p);
+      else if (q.dh.tn == 4) hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<2, 4, 32>), grid, dim3(256), 0, str, p);
+      else if (q.dh.tm == 2) hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<2, 2, 64>), grid, dim3(256), 0, str, p);
+      else hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<1, 2, 64>), grid, dim3(256), 0, str, p);
     }
-    if (dw)
-      hipLaunchKernelGGL((nvfp4::vocab_dw_kernel<4, 2, 32>), nvfp4::tile_grid(nvfp4::tiles_of(p.width, k, 4, 2)),
-                         dim3(256), 0, str, p);
+    if (dw) {
+      const dim3 grid = nvfp4::tile_grid(nvfp4::tiles_of(p.width, k, q.dw.tm, q.dw.tn));
+      if (q.dw.tn == 4) hipLaunchKernelGGL((nvfp4::vocab_dw_kernel<4, 4, 64>), grid, dim3(256), 0, str, p);
+      else if (q.dw.tm == 4) hipLaunchKernelGGL((nvfp4::vocab_dw_kernel<4, 2, 32>), grid, dim3(256), 0, str, p);
+      else hipLaunchKernelGGL((nvfp4::vocab_dw_kernel<2, 2, 64>), grid, dim3(256), 0, str, p);
+    }
   }
   if (dh && rows > 0) {
-    const int64_t blocks = (rows * (k / 8) + 255) / 256;
+    const int64_t blocks = (rows * (k / 8) + 31) / 32;
     if (vocab == 0) p.splits = 0;
     hipLaunchKernelGGL(nvfp4::vocab_dh_join_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, str, p);
   }
