@@ -1009,14 +1009,22 @@ def _disjoint(grads, outs, sizes):
             raise ValueError("out must not overlap another gradient (tensor %d)" % i)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _workspace(t, need, dev, *others):
-    """The caller's workspace, checked, or one of `need` bytes for this call."""
+    """The caller's workspace, checked, or one of `need` bytes for this call:
+    (tensor to hold on to, address, bytes)."""
     if t is None:
-        return torch.empty((need,), dtype=torch.uint8, device=dev)
+        if need == 0:
+            return None, None, 0
+        t = torch.empty((need,), dtype=torch.uint8, device=dev)
+        return t, t.data_ptr(), need
     _dev(t, "workspace", (torch.uint8,), 1)
     _same_device(dev, ("workspace", t))
     _no_overlap(t, "workspace", *others)
-    return t
+    return t, t.data_ptr(), t.numel()
 
 
 def _gate_inputs(logits, experts, valid):
@@ -1050,25 +1058,25 @@ def nvfp4_moe_gate(logits, experts, valid=None, normalize=True, balance=True, ou
     nvfp4_moe_gate_workspace(tokens, experts) bytes.
     """
     T, E, K, dev = _gate_inputs(logits, experts, valid)
-    want = [("weights", (T, K), torch.float32)]
+    want = [("weights", (T, K), logits)]
     if balance:
-        want += [("counts", (E + 1,), torch.int32), ("prob_sums", (E,), torch.float32), ("loss", (), torch.float32)]
+        want += [("counts", (E + 1,), experts), ("prob_sums", (E,), logits), ("loss", (), logits)]
     out = _given(out, "weights", "counts", "prob_sums", "loss")
     res = {}
-    for key, shape, dt in want:
+    for key, shape, like in want:
         t = out.get(key)
         if t is None:
-            res[key] = torch.empty(shape, dtype=dt, device=dev)
+            res[key] = like.new_empty(shape)
             continue
-        res[key] = _out(t, "out " + key, shape, dt, dev)
+        res[key] = _out(t, "out " + key, shape, like.dtype, dev)
         _no_overlap(t, "out " + key, logits, experts, valid, *[o for k, o in res.items() if k != key])
     g = res.get
-    workspace = _workspace(workspace, lib().nvfp4_moe_gate_workspace(T, E) if balance else 0, dev, logits, experts, valid,
-                           *res.values())
+    keep, ws, size = _workspace(workspace, lib().nvfp4_moe_gate_workspace(T, E) if balance else 0, dev, logits, experts,
+                                valid, *res.values())
     with _on(dev):
-        st = lib().nvfp4_moe_gate(_ptr(logits), _ptr(experts), _ptr(valid), T, E, K, int(bool(normalize)),
-                                  _ptr(res["weights"]), _ptr(g("counts")), _ptr(g("prob_sums")), _ptr(g("loss")),
-                                  _ptr(workspace), workspace.numel(), _stream(dev))
+        st = lib().nvfp4_moe_gate(_addr(logits), _addr(experts), _addr(valid), T, E, K, int(bool(normalize)),
+                                  _addr(res["weights"]), _addr(g("counts")), _addr(g("prob_sums")), _addr(g("loss")),
+                                  ws, size, _stream(dev))
     _check("nvfp4_moe_gate", st)
     return res
 
@@ -1101,13 +1109,13 @@ def nvfp4_moe_gate_backward(logits, experts, counts=None, d_weights=None, d_loss
             raise ValueError("counts must have experts + 1 entries")
     _same_device(dev, ("counts", counts), ("d_weights", d_weights), ("d_loss", d_loss))
     if out is None:
-        out = torch.empty((T, E), dtype=torch.float32, device=dev)
+        out = logits.new_empty((T, E))
     else:
         _out(out, "out", (T, E), torch.float32, dev)
         _no_overlap(out, "out", logits, experts, valid, counts, d_weights, d_loss)
     with _on(dev):
-        st = lib().nvfp4_moe_gate_backward(_ptr(logits), _ptr(experts), _ptr(valid), _ptr(counts), T, E, K,
-                                           int(bool(normalize)), _ptr(d_weights), _ptr(d_loss), _ptr(out), _stream(dev))
+        st = lib().nvfp4_moe_gate_backward(_addr(logits), _addr(experts), _addr(valid), _addr(counts), T, E, K,
+                                           int(bool(normalize)), _addr(d_weights), _addr(d_loss), _addr(out), _stream(dev))
     _check("nvfp4_moe_gate_backward", st)
     return out
 
@@ -1128,7 +1136,7 @@ def nvfp4_embedding(table, ids, scale=1.0, out=None, out_dtype=torch.bfloat16):
         _out(out, "out", shape, _out_dtype(out.dtype), dev)
         _no_overlap(out, "out", table, ids)
     with _on(dev):
-        st = lib().nvfp4_embedding(_ptr(table), _type(table), vocab, _ptr(ids), ids.numel(), d, float(scale), _ptr(out),
+        st = lib().nvfp4_embedding(_addr(table), _type(table), vocab, _addr(ids), ids.numel(), d, float(scale), _addr(out),
                                    _type(out), _stream(dev))
     _check("nvfp4_embedding", st)
     return out
@@ -1169,10 +1177,10 @@ def nvfp4_embedding_backward(dout, ids, vocab, scale=1.0, add=None, out=None, ou
             raise TypeError("add must have the output's dtype %s (got %s)" % (out.dtype, add.dtype))
         if add.data_ptr() != out.data_ptr():
             _no_overlap(out, "out", add)
-    workspace = _workspace(workspace, lib().nvfp4_embedding_backward_workspace(n, d), dev, dout, ids, add, out)
+    keep, ws, size = _workspace(workspace, lib().nvfp4_embedding_backward_workspace(n, d), dev, dout, ids, add, out)
     with _on(dev):
-        st = lib().nvfp4_embedding_backward(_ptr(dout), _type(dout), _ptr(ids), n, vocab, d, float(scale), _ptr(add),
-                                            _ptr(out), _type(out), _ptr(workspace), workspace.numel(), _stream(dev))
+        st = lib().nvfp4_embedding_backward(_addr(dout), _type(dout), _addr(ids), n, vocab, d, float(scale), _addr(add),
+                                            _addr(out), _type(out), ws, size, _stream(dev))
     _check("nvfp4_embedding_backward", st)
     return out
 
@@ -1218,10 +1226,11 @@ def nvfp4_vocab_loss(h, w, targets, scale=1.0, out=None, workspace=None):
             continue
         res[key] = _out(t, "out " + key, (rows,), torch.float32, dev)
         _no_overlap(t, "out " + key, h, w, targets, *[o for n, o in res.items() if n != key])
-    workspace = _workspace(workspace, lib().nvfp4_vocab_loss_workspace(rows, vocab, k), dev, h, w, targets, *res.values())
+    keep, ws, size = _workspace(workspace, lib().nvfp4_vocab_loss_workspace(rows, vocab, k), dev, h, w, targets,
+                                *res.values())
     with _on(dev):
-        st = lib().nvfp4_vocab_loss(_ptr(h), _ptr(w), _ptr(targets), rows, vocab, k, float(scale), _ptr(res["loss"]),
-                                    _ptr(res["lse"]), _ptr(workspace), workspace.numel(), _stream(dev))
+        st = lib().nvfp4_vocab_loss(_addr(h), _addr(w), _addr(targets), rows, vocab, k, float(scale), _addr(res["loss"]),
+                                    _addr(res["lse"]), ws, size, _stream(dev))
     _check("nvfp4_vocab_loss", st)
     return res
 
@@ -1273,12 +1282,12 @@ def nvfp4_vocab_loss_backward(h, w, targets, lse, d_loss, scale=1.0, add=None, w
             same = add is not None and add.data_ptr() == t.data_ptr()
             _no_overlap(t, "out dw", h, w, targets, lse, d_loss, None if same else add, res.get("dh"))
         res["dw"] = t
-    workspace = _workspace(workspace, lib().nvfp4_vocab_loss_backward_workspace(rows, vocab, k), dev, h, w, targets, lse,
-                           d_loss, add, *res.values())
     dw = res.get("dw")
     with _on(dev):
-        st = lib().nvfp4_vocab_loss_backward(_ptr(h), _ptr(w), _ptr(targets), _ptr(lse), _ptr(d_loss), rows, vocab, k,
-                                             float(scale), _ptr(add), _ptr(res.get("dh")), _ptr(dw),
-                                             _type(dw), _ptr(workspace), workspace.numel(), _stream(dev))
+        keep, ws, size = _workspace(workspace, lib().nvfp4_vocab_loss_backward_workspace(rows, vocab, k), dev, h, w, targets,
+                                    lse, d_loss, add, *res.values())
+        st = lib().nvfp4_vocab_loss_backward(_addr(h), _addr(w), _addr(targets), _addr(lse), _addr(d_loss), rows, vocab, k,
+                                             float(scale), _addr(add), _addr(res.get("dh")), _addr(dw),
+                                             _type(dw), ws, size, _stream(dev))
     _check("nvfp4_vocab_loss_backward", st)
     return res

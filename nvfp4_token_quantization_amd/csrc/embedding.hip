@@ -28,7 +28,6 @@ namespace nvfp4 {
 constexpr int EMBED_CHUNK = 2048;  // ids sorted together
 constexpr int EMBED_RANK = 64;     // ids a block of step 1 places, by 16 slices of the chunk
 constexpr int EMBED_MERGE = 128;   // ids a block of step 2 places, by 8 slices of the chunks
-constexpr int EMBED_ROWS = 64;     // table rows a block looks for and fills
 constexpr uint32_t EMBED_NONE = 0x7FFFFFFFu;  // an id outside the table: sorted last
 
 struct EmbedArgs {
@@ -47,6 +46,7 @@ struct EmbedArgs {
   int64_t run;       // sorted tokens a wave adds
   int64_t runs;
   int pieces;        // of 512 columns
+  int fill_rows;     // table rows a block of step 3 looks for and fills, at most 64
 };
 
 __device__ __forceinline__ uint32_t embed_key(const EmbedArgs& p, int64_t i) {
@@ -229,14 +229,24 @@ __global__ __launch_bounds__(1024) void embed_merge_kernel(EmbedArgs p) {
   }
 }
 
-// first place in the sorted ids whose id is not below `id`
-__device__ __forceinline__ int64_t embed_lower(const EmbedArgs& p, uint32_t id) {
+// First place in the sorted ids whose id is not below `id`, which the lanes of
+// each half of the wave share: every round asks for 32 places at a time, where
+// the latency of a load is the time (a binary search over 16384 takes 14 of
+// them, this 3).
+__device__ __forceinline__ int64_t embed_lower(const EmbedArgs& p, uint32_t id, int lane) {
   const uint32_t* key = p.key[p.sorted];
-  int64_t lo = 0, hi = p.tokens;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (key[mid] < id) lo = mid + 1;
-    else hi = mid;
+  const int l = lane & 31;
+  int64_t lo = 0, hi = p.tokens;  // the place is in [lo, hi]
+  while (__ballot(lo < hi)) {
+    const int64_t step = (hi - lo + 31) / 32;
+    const int64_t at = max(min(lo + step * (l + 1), hi) - 1, (int64_t)0);
+    const uint64_t below = __ballot(lo < hi && key[at] < id);
+    const int n = __popc((uint32_t)(lane < 32 ? below : below >> 32));
+    if (lo < hi) {
+      const int64_t first = lo + step * n;
+      hi = n == 32 ? hi : min(lo + step * (n + 1), hi) - 1;
+      lo = min(first, hi);
+    }
   }
   return lo;
 }
@@ -251,23 +261,50 @@ __device__ __forceinline__ void embed_write(const EmbedArgs& p, uint32_t v, int 
   embed_store<C, OUT_BF, 2>(row_at(p.out, OUT_BF, v, p.d), p.d, piece, lane, o);
 }
 
-// Table rows [v0, v0 + EMBED_ROWS) that no token names: zeros, or add.
+// Table rows [v0, v0 + n), n <= 64, that no token names: zeros, or add.  Rows next
+// to each other are one stretch of memory, written 16 bytes a lane but for its
+// ends; WIDE: add lies as out does, so it is read so too.
 template <bool WIDE>
-__device__ __forceinline__ void embed_fill(const EmbedArgs& p, int64_t v0, int tid) {
+__device__ __forceinline__ void embed_fill(const EmbedArgs& p, int64_t v0, int n, int tid) {
   const int lane = tid & 63;
-  const int64_t v = v0 + lane;
-  const int64_t at = v < p.vocab ? embed_lower(p, (uint32_t)v) : p.tokens;
-  const bool named = v >= p.vocab || (at < p.tokens && p.key[p.sorted][at] == (uint32_t)v);
+  const int64_t end = embed_lower(p, (uint32_t)(v0 + (lane < 32 ? 0 : n)), lane);
+  int64_t lo = __shfl(end, 0, 64), hi = __shfl(end, 63, 64);  // places of the rows' tokens
+  const uint32_t* key = p.key[p.sorted];
+  const uint32_t v = (uint32_t)v0 + lane;
+  const int64_t last = hi;
+  while (__ballot(lo < hi)) {
+    const int64_t mid = (lo + hi) / 2;
+    if (lo < hi) {
+      if (key[mid] < v) lo = mid + 1;
+      else hi = mid;
+    }
+  }
+  const bool named = lane >= n || (lo < last && key[lo] == v);
   uint64_t fill = ~__ballot(named);
-  typedef typename std::conditional<WIDE, u32x4, uint16_t>::type word;
-  const int64_t n = p.d * (p.out_bf ? 2 : 4) / (int64_t)sizeof(word);  // of a row
-  const word* add = static_cast<const word*>(p.add);
-  word* out = static_cast<word*>(p.out);
+  const int64_t rowb = p.d * (p.out_bf ? 2 : 4);
+  uint8_t* out = static_cast<uint8_t*>(p.out);
+  const uint8_t* add = static_cast<const uint8_t*>(p.add);
   while (fill) {
-    const int64_t row = v0 + __builtin_ctzll(fill);
-    fill &= fill - 1;
-    for (int64_t i = row * n + tid; i < (row + 1) * n; i += 256)
-      __builtin_nontemporal_store(add ? __builtin_nontemporal_load(add + i) : word{}, out + i);
+    const int r = __builtin_ctzll(fill);
+    const uint64_t rest = ~(fill >> r);
+    const int rows = rest ? __builtin_ctzll(rest) : 64;
+    fill = r + rows < 64 ? fill & (~0ull << (r + rows)) : 0;
+    const int64_t b0 = (v0 + r) * rowb, b1 = b0 + rows * rowb;  // bytes of the stretch, and whole pieces within
+    const int64_t skip = (16 - ((int64_t)(uintptr_t)(out + b0) & 15)) & 15;
+    const int64_t w0 = min(b0 + skip, b1), w1 = w0 + (b1 - w0) / 16 * 16;
+    if (!add || WIDE)
+      for (int64_t i = w0 + 16 * tid; i < w1; i += 16 * 256) {
+        u32x4 x = {};
+        if (add) x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(add + i));
+        __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(out + i));
+      }
+    else
+      for (int64_t i = w0 + 2 * tid; i < w1; i += 2 * 256)
+        *reinterpret_cast<uint16_t*>(out + i) = *reinterpret_cast<const uint16_t*>(add + i);
+    // the ends, under 16 bytes each, by 8 threads each
+    const int64_t i = tid < 8 ? b0 + 2 * tid : w1 + 2 * (tid - 8);
+    if (tid < 16 && i < (tid < 8 ? w0 : b1))
+      *reinterpret_cast<uint16_t*>(out + i) = add ? *reinterpret_cast<const uint16_t*>(add + i) : (uint16_t)0;
   }
 }
 
@@ -277,7 +314,8 @@ template <int C, bool IN_BF, bool OUT_BF, bool WIDE>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs p, int64_t sum_blocks) {
   const int tid = threadIdx.x, lane = tid & 63;
   if (blockIdx.x >= sum_blocks) {
-    embed_fill<WIDE>(p, (int64_t)(blockIdx.x - sum_blocks) * EMBED_ROWS, tid);
+    const int64_t v0 = (int64_t)(blockIdx.x - sum_blocks) * p.fill_rows;
+    embed_fill<WIDE>(p, v0, (int)min((int64_t)p.fill_rows, p.vocab - v0), tid);
     return;
   }
   const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -322,41 +360,72 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs p, int64_t sum
   }
 }
 
-// Block (b, piece): the run that starts in b's tokens and goes on past them.
-constexpr int EMBED_JOIN = 8;  // waves that share the partial rows
-template <int C, bool OUT_BF>
-__global__ __launch_bounds__(64 * EMBED_JOIN) void embed_join_kernel(EmbedArgs p) {
-  __shared__ float s_sum[EMBED_JOIN][8][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t b = blockIdx.x / p.pieces;
-  const int piece = (int)(blockIdx.x % p.pieces);
-  const uint32_t* key = p.key[p.sorted];
-  const int64_t i0 = b * p.run, i1 = i0 + p.run;  // i1 < tokens: the last block is not launched
-  const uint32_t id = key[i1 - 1];
-  if (id == EMBED_NONE || key[i1] != id || (i0 > 0 && key[i0 - 1] == id)) return;  // block-uniform
-  const int64_t last = (embed_lower(p, id + 1) - 1) / p.run;  // block of its last token
-  float sum[8] = {};
-  if (wave == 0) embed_load<C, false>(p.part + (2 * b + 1) * p.d, p.d, piece, lane, sum);
-  const int64_t rows = last - b, per = (rows + EMBED_JOIN - 1) / EMBED_JOIN, end = min(rows, (wave + 1) * per);
-  for (int64_t g = wave * per; g < end; g += EMBED_AHEAD) {
+// The runs that start in the tokens of one of a block's 16 waves of step 3 and go
+// on past them, a wave a run: its first partial row and those of the waves that
+// it goes on through.  Long runs are left for all 16 waves together.
+constexpr int EMBED_JOIN = 16;
+constexpr int EMBED_LONG = 2 * EMBED_AHEAD;  // partial rows that a wave adds alone
+template <int C>
+__device__ __forceinline__ void embed_add_parts(const EmbedArgs& p, int64_t b, int64_t from, int64_t to, int piece, int lane,
+                                                float (&sum)[8]) {
+  for (int64_t g = from; g < to; g += EMBED_AHEAD) {
     float v[EMBED_AHEAD][8];
 #pragma unroll
     for (int k = 0; k < EMBED_AHEAD; ++k)
-      embed_load<C, false>(p.part + 2 * (b + 1 + min(g + k, end - 1)) * p.d, p.d, piece, lane, v[k]);
+      embed_load<C, false>(p.part + 2 * (b + 1 + min(g + k, to - 1)) * p.d, p.d, piece, lane, v[k]);
 #pragma unroll
     for (int k = 0; k < EMBED_AHEAD; ++k)
-      if (g + k < end)
+      if (g + k < to)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += v[k][e];
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) s_sum[wave][e][lane] = sum[e];
+}
+template <int C, bool OUT_BF>
+__global__ __launch_bounds__(64 * EMBED_JOIN) void embed_join_kernel(EmbedArgs p) {
+  __shared__ float s_sum[EMBED_JOIN][8][64];
+  __shared__ int s_rows[EMBED_JOIN];  // partial rows of a wave's long run, 0: none
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t b0 = (int64_t)(blockIdx.x / p.pieces) * EMBED_JOIN;
+  const int piece = (int)(blockIdx.x % p.pieces);
+  const uint32_t* key = p.key[p.sorted];
+  {
+    const int64_t b = b0 + wave, i0 = b * p.run, i1 = i0 + p.run;
+    int64_t rows = 0;
+    uint32_t id = EMBED_NONE;
+    if (i1 < p.tokens) {  // there is a wave after it
+      const uint32_t before = i0 > 0 ? key[i0 - 1] : EMBED_NONE, after = key[i1];
+      id = __builtin_amdgcn_readfirstlane(key[i1 - 1]);
+      if (id != EMBED_NONE && after == id && before != id)
+        rows = __shfl((embed_lower(p, id + 1, lane) - 1) / p.run, 0, 64) - b;
+    }
+    if (lane == 0) s_rows[wave] = rows > EMBED_LONG ? (int)rows : 0;
+    if (rows > 0 && rows <= EMBED_LONG) {
+      float sum[8];
+      embed_load<C, false>(p.part + (2 * b + 1) * p.d, p.d, piece, lane, sum);
+      embed_add_parts<C>(p, b, 0, rows, piece, lane, sum);
+      embed_write<C, OUT_BF>(p, id, piece, lane, sum);
+    }
+  }
   __syncthreads();
-  if (wave) return;
-  for (int w = 1; w < EMBED_JOIN; ++w)
+  for (int w = 0; w < EMBED_JOIN; ++w) {
+    const int rows = s_rows[w];
+    if (rows == 0) continue;  // block-uniform
+    const int64_t b = b0 + w;
+    float sum[8] = {};
+    if (wave == 0) embed_load<C, false>(p.part + (2 * b + 1) * p.d, p.d, piece, lane, sum);
+    const int64_t per = (rows + EMBED_JOIN - 1) / EMBED_JOIN;
+    embed_add_parts<C>(p, b, wave * per, min((int64_t)rows, (wave + 1) * per), piece, lane, sum);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] += s_sum[w][e][lane];
-  embed_write<C, OUT_BF>(p, id, piece, lane, sum);
+    for (int e = 0; e < 8; ++e) s_sum[wave][e][lane] = sum[e];
+    __syncthreads();
+    if (wave == 0) {
+      for (int o = 1; o < EMBED_JOIN; ++o)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += s_sum[o][e][lane];
+      embed_write<C, OUT_BF>(p, __builtin_amdgcn_readfirstlane(key[(b + 1) * p.run - 1]), piece, lane, sum);
+    }
+    __syncthreads();
+  }
 }
 
 // rows of `d` elements that lie on 16-byte (bf16: C = 4, 8-byte) pieces of C elements
@@ -371,17 +440,18 @@ static void embed_types(bool in_bf, bool out_bf, F&& f) {
   else f(std::false_type(), std::false_type());
 }
 
-// Sorted tokens a wave adds: 64 at most (its lanes hold their ids), and fewer
-// where that leaves CUs without a wave.
-static int64_t embed_run(int64_t tokens, int64_t pieces) {
-  int64_t run = 64;
-  while (run > 8 && tokens * pieces < run * 4 * 256) run /= 2;
+// Sorted tokens a wave adds, a power of two from 8 to 64 (its lanes hold their
+// ids).  A wave adds 8 at a time, and where one id takes all tokens 16 waves join
+// 8 partial rows each at a time: run / 8 + tokens / (128 run) rounds are least at
+// run^2 = tokens / 16.
+static int64_t embed_run(int64_t tokens) {
+  int64_t run = 8;
+  while (run < 64 && 2 * run * run * 16 < tokens) run *= 2;
   return run;
 }
 
 static int64_t embed_bytes(int64_t tokens, int64_t d) {
-  const int64_t pieces = (d + 511) / 512, run = embed_run(tokens, pieces);
-  const int64_t runs = (tokens + run - 1) / run, lists = (tokens + 3) / 4 * 4;
+  const int64_t run = embed_run(tokens), runs = (tokens + run - 1) / run, lists = (tokens + 3) / 4 * 4;
   return 4 * 4 * lists + (runs > 1 ? runs * 2 * d * 4 : 0);
 }
 
@@ -448,7 +518,7 @@ extern "C" int nvfp4_embedding_backward(const void* dout, int dout_type, const i
   p.ids = ids; p.in = dout; p.add = add; p.out = dtable; p.tokens = tokens; p.vocab = vocab; p.d = d; p.scale = scale;
   p.in_bf = dout_type == NVFP4_TYPE_BF16; p.out_bf = dtable_type == NVFP4_TYPE_BF16;
   p.pieces = (int)((d + 511) / 512);
-  p.run = nvfp4::embed_run(tokens, p.pieces);
+  p.run = nvfp4::embed_run(tokens);
   p.runs = (tokens + p.run - 1) / p.run;
   const int64_t lists = (tokens + 3) / 4 * 4;
   int32_t* ws = static_cast<int32_t*>(workspace);
@@ -469,9 +539,11 @@ extern "C" int nvfp4_embedding_backward(const void* dout, int dout_type, const i
                          dim3(1024), 0, str, p);
   }
   const int64_t sum_blocks = (p.runs * p.pieces + 3) / 4;
-  const int64_t fill_blocks = add == dtable ? 0 : (vocab + nvfp4::EMBED_ROWS - 1) / nvfp4::EMBED_ROWS;
-  const dim3 grid((unsigned)(sum_blocks + fill_blocks)), join((unsigned)((p.runs - 1) * p.pieces));
-  const bool wide = d * (p.out_bf ? 2 : 4) % 16 == 0 && aligned(dtable, 16) && aligned(add, 16);
+  // few rows of a small table a block, so that the fill is spread over the CUs
+  p.fill_rows = vocab >= 64 * 1024 ? 64 : vocab >= 16 * 1024 ? 16 : 4;
+  const int64_t fill_blocks = add == dtable ? 0 : (vocab + p.fill_rows - 1) / p.fill_rows;
+  const dim3 grid((unsigned)(sum_blocks + fill_blocks)), join((unsigned)((p.runs + nvfp4::EMBED_JOIN - 1) / nvfp4::EMBED_JOIN * p.pieces));
+  const bool wide = ((uintptr_t)add & 15) == ((uintptr_t)dtable & 15);
   nvfp4::embed_types(p.in_bf, p.out_bf, [&](auto in, auto o) {
     constexpr bool IN = decltype(in)::value, OUT = decltype(o)::value;
     auto launch = [&](auto c, auto w) {

@@ -47,6 +47,13 @@ struct GateArgs {
   float* d_logits;
 };
 
+// e^d for d <= 0 by the hardware's power of two: log2(e) in two parts, so that the
+// argument keeps its 24 bits (a power below 2^-126 comes out as zero)
+__device__ __forceinline__ float gate_exp(float d) {
+  constexpr float HI = 0x1.715476p+0f, LO = 0x1.4ae0cp-26f;
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(d, HI, d * LO));
+}
+
 // sum or max over aligned groups of L lanes (every lane gets it), a fixed tree
 template <int L, class F>
 __device__ __forceinline__ float group_reduce(float v, F&& f) {
@@ -142,12 +149,13 @@ __device__ __forceinline__ void gate_weights(const GateArgs& p, const GateChoice
   float sum = 0.0f;
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    w[q] = c.e[q] >= 0 ? expf(c.x[q] - m) : 0.0f;
+    w[q] = c.e[q] >= 0 ? gate_exp(c.x[q] - m) : 0.0f;
     sum += w[q];
   }
   if (p.normalize) s = group_sum<L>(sum);
+  const float r = 1.0f / s;
 #pragma unroll
-  for (int q = 0; q < Q; ++q) w[q] = c.e[q] >= 0 ? w[q] / s : 0.0f;
+  for (int q = 0; q < Q; ++q) w[q] = c.e[q] >= 0 ? w[q] * r : 0.0f;
 }
 
 // the lane's logits x to their softmax over the token's (0 past E)
@@ -160,12 +168,13 @@ __device__ __forceinline__ void gate_softmax(const GateArgs& p, int j, float (&x
   s = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    x[v] = j + L * v < p.E ? expf(x[v] - m) : 0.0f;
+    x[v] = j + L * v < p.E ? gate_exp(x[v] - m) : 0.0f;
     s += x[v];
   }
   s = group_sum<L>(s);
+  const float r = 1.0f / s;
 #pragma unroll
-  for (int v = 0; v < V; ++v) x[v] = x[v] / s;
+  for (int v = 0; v < V; ++v) x[v] *= r;
 }
 
 template <int L, int V, bool BALANCE>
