@@ -793,8 +793,8 @@ extern "C" int nvfp4_vocab_loss(const uint16_t* h, const uint16_t* w, const int3
   if (st) return st;
   if (rows == 0) return NVFP4_SUCCESS;
   if (!targets || !loss || !lse || (k > 0 && (!h || (vocab > 0 && !w)))) return NVFP4_ERROR_INVALID_VALUE;
-  if (!workspace || workspace_bytes < nvfp4_vocab_loss_workspace(rows, vocab, k)) return NVFP4_ERROR_INVALID_VALUE;
   if (!nvfp4::tile_grid_ok(rows, 0, vocab)) return NVFP4_ERROR_UNSUPPORTED_SHAPE;
+  if (!workspace || workspace_bytes < nvfp4_vocab_loss_workspace(rows, vocab, k)) return NVFP4_ERROR_INVALID_VALUE;
   if (!aligned(h, 16) || !aligned(w, 16) || !aligned(targets, 4) || !aligned(loss, 4) || !aligned(lse, 4) ||
       !aligned(workspace, 16))
     return NVFP4_ERROR_MISALIGNED;
@@ -835,10 +835,10 @@ extern "C" int nvfp4_vocab_loss_backward(const uint16_t* h, const uint16_t* w, c
   if (k == 0 || (rows == 0 && (vocab == 0 || !dw))) return NVFP4_SUCCESS;
   if (rows > 0 && (!h || !targets || !lse || !d_loss)) return NVFP4_ERROR_INVALID_VALUE;
   if (vocab > 0 && !w) return NVFP4_ERROR_INVALID_VALUE;
-  if (!workspace || workspace_bytes < nvfp4_vocab_loss_backward_workspace(rows, vocab, k)) return NVFP4_ERROR_INVALID_VALUE;
   const nvfp4::VocabPlan q = nvfp4::vocab_plan(rows, vocab, k);
   if (!nvfp4::tile_grid_ok(rows, 0, vocab) || !nvfp4::tile_grid_ok(vocab, 0, k) || !nvfp4::tile_grid_ok(rows * q.splits, 0, k))
     return NVFP4_ERROR_UNSUPPORTED_SHAPE;
+  if (!workspace || workspace_bytes < nvfp4_vocab_loss_backward_workspace(rows, vocab, k)) return NVFP4_ERROR_INVALID_VALUE;
   if (!aligned(h, 16) || !aligned(w, 16) || !aligned(targets, 4) || !aligned(lse, 4) || !aligned(d_loss, 4) ||
       !aligned(add, 16) || !aligned(dh, 16) || !aligned(dw, 16) || !aligned(workspace, 16))
     return NVFP4_ERROR_MISALIGNED;
