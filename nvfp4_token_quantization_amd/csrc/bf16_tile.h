@@ -53,12 +53,9 @@ __device__ __forceinline__ int bg_col_swz(int r) {
   return TN == 1 ? (r & 2) << 1 : ((r & 3) << 2) ^ (r & 2);
 }
 
-// The same for 16 x 16 x 32 fragments, whose lanes 16 .. 31 read rows 8 further
-// on: those take the other 32 bytes of each 64.
-template <int TN>
-__device__ __forceinline__ int bg_col_swz16(int r) {
-  return (TN == 1 ? (r & 2) << 1 : (r & 3) << 2) ^ ((r >> 2) & 2);
-}
+// The same for 16 x 16 x 32 fragments of 2 or more slabs, whose lanes 16 .. 31
+// read rows 8 further on: those take the other 32 bytes of each 64.
+__device__ __forceinline__ int bg_col_swz16(int r) { return ((r & 3) << 2) ^ ((r >> 2) & 2); }
 
 template <int MODE> struct BgMode {
   static constexpr bool a_cols = MODE == BG_WGRAD;     // A is a column operand
@@ -119,7 +116,7 @@ template <int T>
 __device__ __forceinline__ bf16x8 bg_frag16_cols(uint8_t* st, int sl, int sub, int t, int lane) {
   const int i = lane & 15, r4 = i >> 2;
   const int row = 32 * t + 8 * (lane >> 4) + r4;
-  const int chunk = (4 * sl + 2 * sub + ((i & 3) >> 1)) ^ bg_col_swz16<T>(row);
+  const int chunk = (4 * sl + 2 * sub + ((i & 3) >> 1)) ^ bg_col_swz16(row);
   uint8_t* p = st + row * (128 * T) + chunk * 16 + (i & 1) * 8;
   typedef __attribute__((address_space(3))) s16x4* lds4;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)p);
@@ -143,10 +140,16 @@ template <int SH> struct BgShape;
 template <> struct BgShape<32> {
   typedef f32x16 acc;
   static constexpr int F = 1, KS = 16;
+  static __device__ __forceinline__ acc mma(bf16x8 a, bf16x8 b, acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
 };
 template <> struct BgShape<16> {
   typedef f32x4 acc;
   static constexpr int F = 2, KS = 32;
+  static __device__ __forceinline__ acc mma(bf16x8 a, bf16x8 b, acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
 };
 
 // Blocks of a tile shape that share a CU's 160 KiB, and the LDS each gets:
@@ -281,8 +284,7 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
 #pragma unroll
     for (int m = 0; m < S; ++m) {
       const int i = m / FN, j = m % FN;
-      if constexpr (SH == 32) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-      else acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      acc[i][j] = BgShape<SH>::mma(fa[i], fb[j], acc[i][j]);
 #pragma unroll
       for (int k = m * items / S; k < (m + 1) * items / S; ++k) item(k);
       __builtin_amdgcn_sched_barrier(0);
@@ -296,8 +298,7 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
     constexpr int S = FA * FN, H = S * 3 / 4, DMAS = decltype(dmas)::value;
     static_for<S>([&](auto mc) __attribute__((always_inline)) {
       constexpr int m = decltype(mc)::value, i = m / FN, j = m % FN;
-      if constexpr (SH == 32) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-      else acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      acc[i][j] = BgShape<SH>::mma(fa[i], fb[j], acc[i][j]);
       if constexpr (m < H) {
         constexpr int k0 = m * READS / H, k1 = (m + 1) * READS / H;
         static_for<k1 - k0>([&](auto k) __attribute__((always_inline)) {
@@ -335,25 +336,23 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
 #pragma unroll
     for (int k = 0; k < READS; ++k) read_one(0, t, fa[t], fb[t], k);
   int cur = 0;
-  // Stage s, whose first fragments are in set `first`; leaves those of the next
-  // stage in set `first + NT` (of two).
+  // 16 x 16 x 32, no gathered rows: stage s, whose first fragments are in set SET;
+  // leaves those of the next stage in set SET + NT (of two).
   auto stage = [&](auto set, int s) __attribute__((always_inline)) {
     constexpr int SET = decltype(set)::value;
     const int nxt = cur + 1 == NB ? 0 : cur + 1;
-    if (gather) gather_rows(s + NB, idx);
 #pragma unroll
     for (int t = 0; t < NT - 1; ++t)
       mma_early(fa[(SET + t) & 1], fb[(SET + t) & 1],
-                [&](int k) __attribute__((always_inline)) { read_one(cur, t + 1, fa[(SET + t + 1) & 1], fb[(SET + t + 1) & 1], k); }, std::integral_constant<int, 0>(), [](int) {});
+                [&](int k) __attribute__((always_inline)) { read_one(cur, t + 1, fa[(SET + t + 1) & 1], fb[(SET + t + 1) & 1], k); },
+                std::integral_constant<int, 0>(), [](int) {});
     wait_lgkmcnt0();
-    if (gather) wait_vmcnt<(NB - 2) * (NC + 1)>();
-    else wait_vmcnt<(NB - 2) * NC>();
+    wait_vmcnt<(NB - 2) * NC>();
     asm volatile("s_barrier" ::: "memory");
     const Issue q = issue_at(s + NB, cur);
     mma_early(fa[(SET + NT - 1) & 1], fb[(SET + NT - 1) & 1],
-              [&](int k) __attribute__((always_inline)) { read_one(nxt, 0, fa[(SET + NT) & 1], fb[(SET + NT) & 1], k); }, std::integral_constant<int, NC>(),
-              [&](int k) __attribute__((always_inline)) { issue_one(q, idx, k); });
-    if (gather) issue_index(s + 2 * NB);
+              [&](int k) __attribute__((always_inline)) { read_one(nxt, 0, fa[(SET + NT) & 1], fb[(SET + NT) & 1], k); },
+              std::integral_constant<int, NC>(), [&](int k) __attribute__((always_inline)) { issue_one(q, idx, k); });
     cur = nxt;
   };
   constexpr std::integral_constant<int, 0> s0{};
@@ -366,31 +365,32 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
       stage(s0, s);
       stage(s1, s + 1);
     }
-  } else
-  for (int s = 0; s < nst; ++s) {
-    const int nxt = cur + 1 == NB ? 0 : cur + 1;
-    if (gather) gather_rows(s + NB, idx);
+  } else {
+    for (int s = 0; s < nst; ++s) {
+      const int nxt = cur + 1 == NB ? 0 : cur + 1;
+      if (gather) gather_rows(s + NB, idx);
 #pragma unroll
-    for (int t = 0; t < NT - LOOK; ++t)
-      mma(fa[t % FB], fb[t % FB], READS,
-          [&](int k) { read_one(cur, t + LOOK, fa[(t + LOOK) % FB], fb[(t + LOOK) % FB], k); });
-    // every read of stage s has landed and stage s + 1 is there: after the
-    // barrier, for all four waves
-    wait_lgkmcnt0();
-    if (gather) wait_vmcnt<(NB - 2) * (NC + 1)>();
-    else wait_vmcnt<(NB - 2) * NC>();
-    asm volatile("s_barrier" ::: "memory");
-    const Issue q = issue_at(s + NB, cur);
+      for (int t = 0; t < NT - LOOK; ++t)
+        mma(fa[t % FB], fb[t % FB], READS,
+            [&](int k) { read_one(cur, t + LOOK, fa[(t + LOOK) % FB], fb[(t + LOOK) % FB], k); });
+      // every read of stage s has landed and stage s + 1 is there: after the
+      // barrier, for all four waves
+      wait_lgkmcnt0();
+      if (gather) wait_vmcnt<(NB - 2) * (NC + 1)>();
+      else wait_vmcnt<(NB - 2) * NC>();
+      asm volatile("s_barrier" ::: "memory");
+      const Issue q = issue_at(s + NB, cur);
 #pragma unroll
-    for (int u = 0; u < LOOK; ++u) {
-      const int t = NT - LOOK + u, d0 = NC * u / LOOK, d1 = NC * (u + 1) / LOOK;
-      mma(fa[t % FB], fb[t % FB], READS + d1 - d0, [&](int k) {
-        if (k < READS) read_one(nxt, u, fa[u], fb[u], k);
-        else issue_one(q, idx, d0 + k - READS);
-      });
+      for (int u = 0; u < LOOK; ++u) {
+        const int t = NT - LOOK + u, d0 = NC * u / LOOK, d1 = NC * (u + 1) / LOOK;
+        mma(fa[t % FB], fb[t % FB], READS + d1 - d0, [&](int k) {
+          if (k < READS) read_one(nxt, u, fa[u], fb[u], k);
+          else issue_one(q, idx, d0 + k - READS);
+        });
+      }
+      if (gather) issue_index(s + 2 * NB);
+      cur = nxt;
     }
-    if (gather) issue_index(s + 2 * NB);
-    cur = nxt;
   }
   wait_lgkmcnt0();
   wait_vmcnt<0>();

@@ -17,7 +17,8 @@
 // the tiles start.  Then no tile needs its maximum first (a reduction across
 // lanes as long as the sum's) and no term that matters can vanish, since lse
 // >= z[r, t_r].  Where a tile's sum leaves fp32 all the same (a logit 88 above
-// the target's), that tile takes its own maximum instead.
+// the target's), that tile takes its own maximum instead.  Up to 64 rows are
+// taken from h by the tiles themselves, each with its own maxima.
 //
 // Backward, a piece of the vocabulary at a time: the logits' tiles again, now
 // turned into dz and rounded to bf16 for the two products that read them (a
@@ -232,10 +233,12 @@ __device__ __forceinline__ RowTerms row_terms(const VocabArgs& p, int64_t row, i
 
 // Partial sums of the tile's rows over its columns, relative to the rows'
 // references (s_ref, of the tile's rows): exponent and sum to p.part[n].  s_part:
-// LDS for 2 x 64 TM of them.
-template <int VS, int TM, int TN>
-__device__ __forceinline__ void tile_part(const VocabArgs& p, const Acc<VS, TN>& acc, const float* s_ref, float2* s_part,
-                                          int64_t row_lo, int64_t row_hi, int64_t n, int w, int lane) {
+// LDS for 2 x 64 TM of them.  OWN: no reference is known, every sum is relative to
+// its row's maximum here, and the tile that holds a row's target (s_col, its
+// column) leaves the reference.
+template <int VS, int TM, int TN, bool OWN = false>
+__device__ __forceinline__ void tile_part(const VocabArgs& p, const Acc<VS, TN>& acc, const float* s_ref, const int* s_col,
+                                          float2* s_part, int64_t row_lo, int64_t row_hi, int64_t n, int w, int lane) {
   constexpr int BM = 64 * TM, BN = 64 * TN;
   const int c16 = lane & 15, q16 = lane >> 4, wr = w >> 1, wc = w & 1;
   const float f = p.scale * LOG2E;
@@ -244,9 +247,10 @@ __device__ __forceinline__ void tile_part(const VocabArgs& p, const Acc<VS, TN>&
 #pragma unroll
   for (int a = 0; a < 2 * VS; ++a) {
     const int row0 = 32 * (2 * (a / 2) + wr) + 16 * (a % 2) + 4 * q16;
-    const f32x4 ref = *reinterpret_cast<const f32x4*>(s_ref + row0);
+    f32x4 ref = {0, 0, 0, 0};
+    if (!OWN) ref = *reinterpret_cast<const f32x4*>(s_ref + row0);
     float s[4] = {}, top[4];
-    bool over = false;
+    bool over = OWN;
     auto sum = [&](auto all) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -256,13 +260,22 @@ __device__ __forceinline__ void tile_part(const VocabArgs& p, const Acc<VS, TN>&
           s[r] += decltype(all)::value || 16 * b < left ? e : 0.0f;
         }
     };
-    if (whole) sum(std::true_type());
-    else sum(std::false_type());
+    if (!OWN) {
+      if (whole) sum(std::true_type());
+      else sum(std::false_type());
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      top[r] = ref[r];
-      s[r] = sum16(s[r]);
-      over |= !(s[r] < 0x1p120f);
+      for (int r = 0; r < 4; ++r) {
+        top[r] = ref[r];
+        s[r] = sum16(s[r]);
+        over |= !(s[r] < 0x1p120f);
+      }
+    } else {
+      const i32x4 col = *reinterpret_cast<const i32x4*>(s_col + row0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int b = 0; b < 2 * TN; ++b)
+          if (col[r] == 32 * TN * wc + 16 * b + c16) p.ref[row_lo + row0 + r] = acc[a][b][r] * f;
     }
     if (__ballot(over)) {  // wave-uniform: such a row's sum relative to its maximum here
 #pragma unroll
@@ -278,7 +291,7 @@ __device__ __forceinline__ void tile_part(const VocabArgs& p, const Acc<VS, TN>&
         }
         u = sum16(u);
         // of this row alone: its neighbours keep their bits
-        if (!(s[r] < 0x1p120f)) {
+        if (OWN || !(s[r] < 0x1p120f)) {
           s[r] = u;
           top[r] = t;
         }
@@ -429,7 +442,7 @@ __device__ __forceinline__ void cols_operand(BgOperand<T>& o, int64_t cols, int 
 #pragma unroll
   for (int i = 0; i < T * BK / 32; ++i) {
     const int row = (4 * i + w) * (8 / T) + lane / (8 * T);
-    const int c = 8 * ((lane % (8 * T)) ^ bg_col_swz16<T>(row));
+    const int c = 8 * ((lane % (8 * T)) ^ bg_col_swz16(row));
     o.voff[i] = c < cols ? (uint32_t)(row * o.stride) + 2 * c : BG_OOB;
   }
 }
@@ -502,7 +515,58 @@ __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_logits_kerne
     }
     __syncthreads();
     if constexpr (DZ) tile_dz<VS, TN>(p, acc, s_ref, s_coef, s_col, lds + 4096, tl.row_lo, tl.row_hi, n, w, lane);
-    else tile_part<VS, TM, TN>(p, acc, s_ref, reinterpret_cast<float2*>(lds + 4096), tl.row_lo, tl.row_hi, n, w, lane);
+    else tile_part<VS, TM, TN>(p, acc, s_ref, nullptr, reinterpret_cast<float2*>(lds + 4096), tl.row_lo, tl.row_hi, n, w, lane);
+  });
+}
+
+// Forward for up to 64 rows, where the table is the work and a launch for the
+// rows would be 6% of the call (64 rows, 131072 x 2560): every block numbers the
+// rows itself, gathers them from h, and takes its own maxima.
+__global__ __launch_bounds__(256, 2) void vocab_few_kernel(VocabArgs p) {
+  constexpr int TN = 2, BN = 64 * TN, BK = 64;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[bg_lds<1, TN>()];
+  static_assert(bg_bufs<BG_FORWARD, 1, TN, 1>((2 + 2 * TN) * 4096) * (2 + 2 * TN) * 4096 <= 76 * 1024, "room past the ring");
+  int* s_row = reinterpret_cast<int*>(lds + 76 * 1024);
+  int* s_target = s_row + 64;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t target = lane < p.rows ? p.targets[lane] : -1;
+  const bool has = target >= 0 && target < p.vocab;
+  const uint64_t mask = __ballot(has);
+  const int count = __popcll(mask), at = __popcll(mask & ((1ull << lane) - 1));
+  if (w == 0 && has) {
+    s_row[at] = lane;
+    s_target[at] = target;
+    if (blockIdx.x == 0) p.row_index[at] = lane;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.count = count;
+  __syncthreads();
+  int64_t n;
+  if (count == 0 || !vocab_turn((p.width + BN - 1) / BN, n)) return;  // block-uniform
+  BgTile tl = {};
+  BgOperand<1> oa;
+  BgOperand<TN> ob;
+  tl.K = p.k;
+  const uint32_t rowb = (uint32_t)p.k * 2;
+  const int64_t cols = min((int64_t)BN, p.width - n * BN);
+  oa.rsrc = bg_rsrc(p.h, p.rows * rowb);
+  const int swz = 16 * ((lane % 8) ^ bg_row_swz<BK>(8 * w + lane / 8));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = 8 * (4 * i + w) + lane / 8;
+    oa.voff[i] = row < count ? (uint32_t)s_row[row] * rowb + swz : BG_OOB;
+  }
+  ob.rsrc = bg_rsrc(p.w + n * BN * p.k, cols * rowb);
+  rows_operand<TN, BK>(ob, cols, rowb, w, lane);
+  int col = -1;
+  if (threadIdx.x < count) {
+    const int64_t c = s_target[threadIdx.x] - n * BN;
+    col = c >= 0 && c < BN ? (int)c : -1;
+  }
+  tile_sums<BG_FORWARD, 1, TN, BK>(tl, oa, ob, lds, 1, w, lane, [&](auto vs, auto& acc) {
+    int* s_col = reinterpret_cast<int*>(lds);
+    if (threadIdx.x < 64) s_col[threadIdx.x] = col;
+    __syncthreads();
+    tile_part<1, 1, TN, true>(p, acc, nullptr, s_col, reinterpret_cast<float2*>(lds + 4096), 0, count, n, w, lane);
   });
 }
 
@@ -810,8 +874,12 @@ extern "C" int nvfp4_vocab_loss(const uint16_t* h, const uint16_t* w, const int3
   p.hc = reinterpret_cast<uint16_t*>(p.ref + list);
   p.part = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(p.hc) + nvfp4::up(rows * k * 2, 16));
   hipStream_t str = (hipStream_t)stream;
-  launch_rows<true>(p, str);  // no row of an empty vocabulary reads w
-  if (vocab > 0) nvfp4::launch_logits<false>(p, str);
+  if (rows <= 64) {
+    hipLaunchKernelGGL(nvfp4::vocab_few_kernel, nvfp4::tile_grid(nvfp4::forward_tiles(rows, vocab)), dim3(256), 0, str, p);
+  } else {
+    launch_rows<true>(p, str);  // no row of an empty vocabulary reads w
+    if (vocab > 0) nvfp4::launch_logits<false>(p, str);
+  }
   const int64_t tiles = nvfp4::forward_tiles(rows, vocab);
   if (rows > 1024)  // whole 128-byte lines of a tile's partial sums; with few rows more CUs
     hipLaunchKernelGGL(nvfp4::vocab_join_kernel<16>, dim3((unsigned)((rows + 15) / 16)), dim3(1024), 0, str, p, tiles);
