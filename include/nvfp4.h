@@ -600,7 +600,8 @@ int nvfp4_clip_grad_norm(const void* const* grads, void* const* out, const int64
  * least one.  counts are constants of the loss, as forward gave them or summed
  * over several ranks: prob_sums then count against the summed N, and the
  * ranks' losses add up.  Padding tokens get zeros.
- * Softmax and sums in fp32, the loss from its sums in fp64.  An expert whose
+ * Softmax and sums in fp32, the loss from its sums in fp64.  Probabilities
+ * below fp32's normal range (2^-126) may be taken as zero.  An expert whose
  * logit is -infinity has p = 0; NaN or +infinity make their own token's
  * values NaN (and with them prob_sums and loss).  Deterministic (integer
  * counts; float sums in a fixed order).  num_experts <= 1024, topk <= 64 and
@@ -638,8 +639,8 @@ int nvfp4_moe_gate_backward(const float* logits, const int32_t* experts, const u
  *   caller's, 16-byte aligned, free for other use when the call's work has
  *   completed.
  * Sums in fp32, of a row's tokens in an order that depends on ids alone (no
- * atomics); an output is rounded once.  tokens <= 2^24, d <= 2^20, vocab <
- * 2^31 - 1.
+ * atomics); an output is rounded once.  tokens <= 2^24, d <= 2^20, vocab <=
+ * 2^29; backward tokens * d < 2^37.
  * Errors: INVALID_VALUE (sizes, types, null pointers with work, a missing or
  * too small workspace), UNSUPPORTED_SHAPE, MISALIGNED (elements to their size,
  * workspace 16 bytes), ARCH, LAUNCH.
@@ -673,8 +674,9 @@ int nvfp4_embedding_backward(const void* dout, int dout_type, const int32_t* ids
  *   workspace: nvfp4_vocab_loss_workspace(rows, vocab, k) or
  *   nvfp4_vocab_loss_backward_workspace(rows, vocab, k) bytes of the caller's,
  *   16-byte aligned, free for other use when the call's work has completed.
- *   The backward pass goes through the vocabulary in pieces; the workspace
- *   holds dz of one of them.
+ *   It holds the h of the rows with a target, and in the backward pass, which
+ *   goes through the vocabulary in pieces, dz of one of them (about 512 MiB,
+ *   never less than 2048 columns) and fp32 sums of dh.
  * Products of bf16 are exact and summed in fp32, softmax and sums are fp32.
  * dz is rounded once to bf16 for the two products that read it (at most 2^-8
  * of each term), dh and a bf16 dw once more.  A row with a NaN or +infinite
@@ -682,7 +684,8 @@ int nvfp4_embedding_backward(const void* dout, int dout_type, const int32_t* ids
  * and dz below fp32's normal range (2^-126) may be taken as zero.
  * Deterministic: no atomics, and a row's results do not depend on which rows
  * have targets other than through the order of the sums of dw.
- * k % 8 == 0, k <= 2^20, vocab <= 2^24, rows * k < 2^30; scale finite.
+ * k % 8 == 0, k <= 2^20, vocab <= 2^24, rows <= 2^24, and rows * vocab, rows *
+ * k and vocab * k below 2^37; scale finite.
  * Errors: INVALID_VALUE (sizes, types, a scale that is not finite, null
  * pointers with work, a missing or too small workspace), UNSUPPORTED_SHAPE,
  * MISALIGNED (h, w, add, dh, dw and workspace 16 bytes, the rest 4), ARCH,

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(256) void vocab_rows_kernel(VocabArgs p) {
 // along m, m fastest, so that the tiles that an XCD works on at a time share
 // panels of both operands in its L2.
 __device__ __forceinline__ void vocab_tile(int64_t tm, int64_t tn, int64_t t, int64_t& m, int64_t& n) {
-  // at most 2^28 tiles; quotients come from the vector unit, so say that they are uniform
+  // fewer than 2^24 tiles; quotients come from the vector unit, so say that they are uniform
   const uint32_t row = 8 * (uint32_t)tn, band = __builtin_amdgcn_readfirstlane((uint32_t)t / row);
   const uint32_t in = (uint32_t)t - band * row, bh = min(8u, (uint32_t)tm - 8 * band);
   const uint32_t q = __builtin_amdgcn_readfirstlane(in / bh);
@@ -731,6 +731,8 @@ static int64_t tiles_of(int64_t rows, int64_t cols, int TM, int TN) {
 }
 // blocks for `tiles` tiles of one block each: every XCD's share rounded up
 static dim3 tile_grid(int64_t tiles) { return dim3((unsigned)(8 * (tiles / 8 + 1))); }
+// a launch has fewer than 2^32 threads
+static bool grid_ok(int64_t tiles) { return tiles < ((int64_t)1 << 24) - 8; }
 
 // Tile of the logits (64 TM rows by 64 TN columns; measured with k = 1032 or
 // 2048, the dz form).  The large tile reads its operands least, and from two
@@ -829,7 +831,8 @@ using nvfp4host::aligned;
 
 static int vocab_sizes(int64_t rows, int64_t vocab, int64_t k, float scale) {
   if (rows < 0 || vocab < 0 || k < 0 || !(scale - scale == 0.0f)) return NVFP4_ERROR_INVALID_VALUE;
-  if (k % 8 != 0 || k > ((int64_t)1 << 20) || vocab > ((int64_t)1 << 24) || rows > ((int64_t)1 << 24))
+  if (k % 8 != 0 || k > ((int64_t)1 << 20) || vocab > ((int64_t)1 << 24) || rows > ((int64_t)1 << 24) ||
+      !nvfp4::grid_ok(nvfp4::tiles_of(rows, vocab, 4, 4)))
     return NVFP4_ERROR_UNSUPPORTED_SHAPE;
   return NVFP4_SUCCESS;
 }
@@ -857,7 +860,6 @@ extern "C" int nvfp4_vocab_loss(const uint16_t* h, const uint16_t* w, const int3
   if (st) return st;
   if (rows == 0) return NVFP4_SUCCESS;
   if (!targets || !loss || !lse || (k > 0 && (!h || (vocab > 0 && !w)))) return NVFP4_ERROR_INVALID_VALUE;
-  if (!nvfp4::tile_grid_ok(rows, 0, vocab)) return NVFP4_ERROR_UNSUPPORTED_SHAPE;
   if (!workspace || workspace_bytes < nvfp4_vocab_loss_workspace(rows, vocab, k)) return NVFP4_ERROR_INVALID_VALUE;
   if (!aligned(h, 16) || !aligned(w, 16) || !aligned(targets, 4) || !aligned(loss, 4) || !aligned(lse, 4) ||
       !aligned(workspace, 16))
@@ -904,7 +906,8 @@ extern "C" int nvfp4_vocab_loss_backward(const uint16_t* h, const uint16_t* w, c
   if (rows > 0 && (!h || !targets || !lse || !d_loss)) return NVFP4_ERROR_INVALID_VALUE;
   if (vocab > 0 && !w) return NVFP4_ERROR_INVALID_VALUE;
   const nvfp4::VocabPlan q = nvfp4::vocab_plan(rows, vocab, k);
-  if (!nvfp4::tile_grid_ok(rows, 0, vocab) || !nvfp4::tile_grid_ok(vocab, 0, k) || !nvfp4::tile_grid_ok(rows * q.splits, 0, k))
+  if (!nvfp4::grid_ok(nvfp4::tiles_of(rows, k, q.dh.tm, q.dh.tn) * q.splits) ||
+      !nvfp4::grid_ok(nvfp4::tiles_of(q.width, k, q.dw.tm, q.dw.tn)))
     return NVFP4_ERROR_UNSUPPORTED_SHAPE;
   if (!workspace || workspace_bytes < nvfp4_vocab_loss_backward_workspace(rows, vocab, k)) return NVFP4_ERROR_INVALID_VALUE;
   if (!aligned(h, 16) || !aligned(w, 16) || !aligned(targets, 4) || !aligned(lse, 4) || !aligned(d_loss, 4) ||

@@ -201,3 +201,22 @@ def test_a_table_past_four_gigabytes():
     g = nv.nvfp4_embedding_backward(out, ids, vocab, out=table)
     assert torch.equal(g[vocab - 1], out[0] + out[2]) and torch.equal(g[vocab // 2], out[3])
     assert int((g != 0).any(1).sum()) == 4
+
+
+# sorted runs of 2048 are merged by eights: one, two and three times, with runs that are short or missing
+@pytest.mark.parametrize("n", [16384, 16385, 32768 + 2049, 131072, 131073, 300001])
+def test_long_batches_by_permutation(n):
+    """Every id once: each row of the table is its token's, to the bit."""
+    g = torch.Generator().manual_seed(n)
+    ids, dout = torch.randperm(n, generator=g).to(I32).to(DEV), randn(n, 8)
+    got = nv.nvfp4_embedding_backward(dout, ids, n)
+    assert torch.equal(got[ids.long()], dout)
+
+
+@pytest.mark.parametrize("n,vocab", [(40000, 1), (140001, 7000), (140001, 300)])
+@pytest.mark.parametrize("how", ["even", "skewed", "strange"])
+def test_long_batches(n, vocab, how):
+    ids, dout = ids_of(n, vocab, how), randn(n, 8)
+    got = nv.nvfp4_embedding_backward(dout, ids, vocab)
+    close(got, *exact_grad(dout, ids, vocab, 1.0), how)
+    assert torch.equal(got, nv.nvfp4_embedding_backward(dout, ids, vocab))

@@ -136,3 +136,18 @@ def test_binding_refusals():
     for bad in (lambda: nv.nvfp4_moe_gate([1], i), lambda: nv.nvfp4_embedding(None, t), lambda: nv.nvfp4_vocab_loss(b, 3, t)):
         with pytest.raises((TypeError, ValueError)):
             bad()
+
+
+def test_sizes_past_what_a_launch_holds(L):
+    f = caller(L.nvfp4_embedding_backward, "g gt ids n vocab d scale add out ot ws bytes stream",
+               dict(g=A, gt=BF16, ids=A, n=4, vocab=9, d=16, scale=1.0, add=None, out=A, ot=F32, ws=A, bytes=1 << 60, stream=None))
+    assert f(vocab=(1 << 29) + 1) == SHAPE
+    assert f(n=1 << 24, d=1 << 20) == SHAPE
+    f = caller(L.nvfp4_vocab_loss, "h w t rows vocab k scale loss lse ws bytes stream",
+               dict(h=A, w=A, t=A, rows=1 << 20, vocab=1 << 20, k=16, scale=1.0, loss=A, lse=A, ws=A, bytes=1 << 60, stream=None))
+    assert f() == SHAPE  # 2^24 tiles of 256 x 256
+    f = caller(L.nvfp4_vocab_loss_backward, "h w t lse d rows vocab k scale add dh dw dwt ws bytes stream",
+               dict(h=A, w=A, t=A, lse=A, d=A, rows=4, vocab=100, k=16, scale=1.0, add=None, dh=A, dw=A, dwt=F32, ws=A,
+                    bytes=1 << 60, stream=None))
+    assert f(rows=1 << 20, vocab=1 << 20) == SHAPE
+    assert f(rows=1 << 24, k=1 << 20) == SHAPE
