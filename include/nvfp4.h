@@ -675,7 +675,7 @@ int nvfp4_embedding_backward(const void* dout, int dout_type, const int32_t* ids
  *   nvfp4_vocab_loss_backward_workspace(rows, vocab, k) bytes of the caller's,
  *   16-byte aligned, free for other use when the call's work has completed.
  *   It holds the h of the rows with a target, and in the backward pass, which
- *   goes through the vocabulary in pieces, dz of one of them (about 512 MiB,
+ *   goes through the vocabulary in pieces, dz of one of them (about 1 GiB,
  *   never less than 2048 columns) and fp32 sums of dh.
  * Products of bf16 are exact and summed in fp32, softmax and sums are fp32.
  * dz is rounded once to bf16 for the two products that read it (at most 2^-8

@@ -175,6 +175,13 @@ constexpr int bg_bufs(int bytes) {
 // their own, and the first adds the others' tiles in order: false for those
 // others, which hold nothing.  On return every LDS byte from bg_sums() on is
 // free.  p: the arguments' row_index and a_rows.
+//
+// Args with a member `blocks` hold A in blocks of 64 x 64 elements, 128 bytes a
+// row, dz_row bytes from one to the next along its rows and dz_col along its
+// columns: the offsets of oa.voff go from oa.base on, and both strides' steps are
+// taken here.
+template <class Args, class = void> constexpr bool bg_blocked = false;
+template <class Args> constexpr bool bg_blocked<Args, std::void_t<decltype(Args::blocks)>> = true;
 template <int VS, int TN, int KG>
 constexpr int bg_sums() { return (KG - 1) * 4 * VS * TN * 16 * 64 * 4; }  // the other groups' accumulators
 template <int MODE, int TM, int TN, int BK, int KG, int VS, int SH, class Args>
@@ -227,14 +234,20 @@ __device__ __forceinline__ bool bg_sum(const Args& p, const BgTile& tl, BgOperan
     q.soff = (uint32_t)s * (BK * 2);
     q.in = (int64_t)s * BK + chunk8 < tl.K;
     const int64_t left = min((int64_t)BK, max((int64_t)0, tl.K - (int64_t)s * BK));
-    q.ra = M::a_cols ? bg_rsrc(oa.base + (int64_t)s * BK * oa.stride, left * oa.stride) : oa.rsrc;
+    if constexpr (bg_blocked<Args>) {
+      const int64_t first = (int64_t)s * BK;
+      const uint8_t* at = M::a_cols ? oa.base + first / 64 * p.dz_row + first % 64 * 128 : oa.base + first / 64 * p.dz_col + first % 64 * 2;
+      q.ra = bg_rsrc(at, left > 0 ? (TM - 1) * (M::a_cols ? p.dz_col : p.dz_row) + 8192 : 0);
+    } else {
+      q.ra = M::a_cols ? bg_rsrc(oa.base + (int64_t)s * BK * oa.stride, left * oa.stride) : oa.rsrc;
+    }
     q.rb = M::b_cols && !gather ? bg_rsrc(ob.base + (int64_t)s * BK * ob.stride, left * ob.stride) : ob.rsrc;
     return q;
   };
   auto issue_one = [&](const Issue& q, const int32_t (&idx)[NC - NA], int k) __attribute__((always_inline)) {
     if (k < NA) {
       if constexpr (M::a_cols) dma16(q.ra, oa.voff[k], 0, q.at + k * 4096);
-      else dma16(q.ra, q.in ? oa.voff[k] : BG_OOB, q.soff, q.at + k * 4096);
+      else dma16(q.ra, q.in ? oa.voff[k] : BG_OOB, bg_blocked<Args> ? 0 : q.soff, q.at + k * 4096);
       return;
     }
     const int i = k - NA;

@@ -21,12 +21,27 @@
 // taken from h by the tiles themselves, each with its own maxima.
 //
 // Backward, a piece of the vocabulary at a time: the logits' tiles again, now
-// turned into dz and rounded to bf16 for the two products that read them (a
-// relative 2^-9 a term, as every gradient that the bf16 products take), then
-// dh += dz w summed over the pieces in fp32, and dw = dz^T h, which is whole
-// for the piece's rows of w.  Few rows leave few tiles of dh: the sum over the
-// vocabulary is then split over blocks, each with fp32 sums of its own, added
-// in order at the end.
+// turned into dz and rounded to bf16 for the two products that read them (at
+// most a relative 2^-8 a term, as every gradient that the bf16 products take),
+// then dh += dz w summed over the pieces in fp32, and dw = dz^T h, which is whole
+// for the piece's rows of w.  The sum of dh over the vocabulary is split over
+// blocks to fill the CUs, each with fp32 sums of its own, added in order at the
+// end.  dz lies in blocks of 64 x 64, so that either product's stage is a few
+// stretches of 8 KiB: in rows of 128 KiB, a stage of dh was 256 lines in as many
+// pages (dh 2590 us, in rows 3190; below).
+//
+// Measured (8192 rows, 6144 of them with a target, vocabulary 131072, k = 2048:
+// 3.3 TFLOP a product; the library's bf16 products of these sizes take 2428 to
+// 2654 us for the logits, 2570 to 2876 for dz w, 2892 to 3134 for dz^T h):
+//   forward   2830 us: rows 22, logits 2790, join 12
+//   backward  8440 us: rows 24, dz 3060 to 3160, dh 2590, dw 2660, join 88
+// bound by the matrix cores: a 256 x 256 tile takes 1.4 us per 64 of k, 1550
+// TFLOP/s were it all, and 10 us to start and leave its sums, 16 to leave dz.
+// Tried and slower: persistent blocks that load the next tile's first stages
+// under the epilogue (3030 us of logits), BK = 32 (2836), streaming stores of dz
+// (3% of the logits).
+//   64 rows, 131072 x 2560: 129 us, the table read at 5.2 TB/s
+//   301 rows, 32003 x 1032, backward: 130 us, dw 45, dz 38, dh 32
 #include <type_traits>
 
 #include "bf16_tile.h"
@@ -51,8 +66,11 @@ struct VocabArgs {
   float *loss, *lse;
   // backward
   const float *lse_in, *d_loss;
-  uint16_t* dz;      // [rows, ld] of the piece
-  int64_t ld, v0, width;  // the piece: vocabulary rows [v0, v0 + width)
+  // dz of the piece, in blocks of 64 x 64 (rows past a multiple of 64 and columns
+  // past the width are zero): bytes from a block to the next below and beside it
+  uint8_t* dz;
+  int64_t dz_row, dz_col;
+  int64_t v0, width;  // the piece: vocabulary rows [v0, v0 + width)
   float* sums;       // [splits][rows, k]
   int splits;
   int64_t per_split; // vocabulary rows a split sums
@@ -315,7 +333,8 @@ __device__ __forceinline__ void tile_part(const VocabArgs& p, const Acc<VS, TN>&
 
 // dz of the tile, 16 rows of a wave at a time: columns of 16 rows go to LDS (TN
 // KiB a wave) 8 bytes a lane and come back as rows (ds_read_b64_tr_b16), 16 bytes
-// a lane.  Columns past the vocabulary, which the products read, are zero.
+// a lane.  Columns past the vocabulary and rows up to the end of a block, which the
+// products read, are zero.
 template <int VS, int TN>
 __device__ __forceinline__ void tile_dz(const VocabArgs& p, const Acc<VS, TN>& acc, const float* s_ref, const float* s_coef,
                                         const int* s_col, uint8_t* lds, int64_t row_lo, int64_t row_hi, int64_t n, int w,
@@ -324,9 +343,13 @@ __device__ __forceinline__ void tile_dz(const VocabArgs& p, const Acc<VS, TN>& a
   typedef __attribute__((address_space(3))) s16x4* lds4;
   const int c16 = lane & 15, q16 = lane >> 4, wr = w >> 1, wc = w & 1;
   const float f = p.scale * LOG2E;
-  const int64_t col0 = n * (64 * TN) + 32 * TN * wc;
-  const int left = (int)min((int64_t)(64 * TN), p.width - col0) - c16;  // this lane's column of b exists: 16 b < left
+  const int rows = (int)(row_hi - row_lo);
+  const int left = (int)min((int64_t)(64 * TN), p.width - n * (64 * TN) - 32 * TN * wc) - c16;  // this lane's column of b exists: 16 b < left
   uint8_t* t = lds + w * (TN * 1024);
+  // the wave's rows of a block, and its first block
+  static_assert(TN % 2 == 0, "a wave's columns are whole blocks");
+  const uint32_t mine = (32 * wr + c16) * 128 + q16 * 16;
+  uint8_t* blocks = p.dz + row_lo / 64 * p.dz_row + (n * TN + TN / 2 * wc) * p.dz_col;
 #pragma unroll
   for (int a = 0; a < 2 * VS; ++a) {
     const int row0 = 32 * (2 * (a / 2) + wr) + 16 * (a % 2);
@@ -359,9 +382,9 @@ __device__ __forceinline__ void tile_dz(const VocabArgs& p, const Acc<VS, TN>& a
       uint8_t* at = t + (c8 + (c16 >> 2)) * 32 + (c16 & 3) * 8;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)at);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(at + 4 * 32));
-      const s16x8 o = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      const int64_t row = row_lo + row0 + c16, c = col0 + c8;
-      if (row < row_hi && c < p.ld) *reinterpret_cast<s16x8*>(p.dz + row * p.ld + c) = o;
+      s16x8 o = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if (row0 + c16 >= rows) o = (s16x8){};
+      *reinterpret_cast<s16x8*>(blocks + a / 2 * p.dz_row + u / 2 * p.dz_col + (a % 2 * 2048 + u % 2 * 64 + mine)) = o;
     }
     wave_lds_sync();
   }
@@ -447,19 +470,42 @@ __device__ __forceinline__ void cols_operand(BgOperand<T>& o, int64_t cols, int 
   }
 }
 
+// DMA offsets of dz's blocks: T blocks along its rows (sums over columns) or along
+// its columns (sums over rows), the first `n` rows or columns of them.
+template <int T, int BK, bool COLS>
+__device__ __forceinline__ void dz_operand(const VocabArgs& p, BgOperand<T>& o, int64_t n, int w, int lane) {
+#pragma unroll
+  for (int i = 0; i < T * BK / 32; ++i) {
+    if (COLS) {
+      const int row = (4 * i + w) * (8 / T) + lane / (8 * T);
+      const int c = 8 * ((lane % (8 * T)) ^ bg_col_swz16(row));
+      o.voff[i] = c < n ? (uint32_t)(c / 64) * (uint32_t)p.dz_col + row * 128 + c % 64 * 2 : BG_OOB;
+    } else {
+      constexpr int CPR = BK / 8;
+      const int row = 64 / CPR * (4 * i + w) + lane / CPR;
+      const int swz = 16 * ((lane % CPR) ^ bg_row_swz<BK>(64 / CPR * w + lane / CPR));
+      o.voff[i] = row < n ? (uint32_t)(row / 64) * (uint32_t)p.dz_row + row % 64 * 128 + swz : BG_OOB;
+    }
+  }
+}
+
 struct NoGather {  // bg_sum's arguments: no row of these operands is gathered
   static constexpr const int32_t* row_index = nullptr;
   static constexpr int64_t a_rows = 0;
 };
+struct DzBlocks : NoGather {  // A is dz
+  static constexpr bool blocks = true;
+  int64_t dz_row, dz_col;
+};
 
 // The sums of a tile's valid slabs, then epi(VS, acc).
-template <int MODE, int TM, int TN, int BK, class Epi>
-__device__ __forceinline__ void tile_sums(const BgTile& tl, BgOperand<TM>& oa, BgOperand<TN>& ob, uint8_t* lds, int vs,
+template <int MODE, int TM, int TN, int BK, class Args, class Epi>
+__device__ __forceinline__ void tile_sums(const Args& args, const BgTile& tl, BgOperand<TM>& oa, BgOperand<TN>& ob, uint8_t* lds, int vs,
                                           int w, int lane, Epi&& epi) {
   auto run = [&](auto n) {
     constexpr int VS = decltype(n)::value;
     Acc<VS, TN> acc;
-    bg_sum<MODE, TM, TN, BK, 1, VS, 16>(NoGather(), tl, oa, ob, lds, (int)((tl.K + BK - 1) / BK), 0, w, lane, acc);
+    bg_sum<MODE, TM, TN, BK, 1, VS, 16>(args, tl, oa, ob, lds, (int)((tl.K + BK - 1) / BK), 0, w, lane, acc);
     epi(n, acc);
   };
   if constexpr (TM == 4) {
@@ -501,7 +547,7 @@ __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_logits_kerne
   ob.rsrc = bg_rsrc(p.w + (p.v0 + n * BN) * p.k, cols * rowb);
   rows_operand<TN, BK>(ob, cols, rowb, w, lane);
   const RowTerms mine = row_terms<DZ>(p, tl.row_lo + threadIdx.x, tl.row_hi, n * BN, BN);
-  tile_sums<BG_FORWARD, TM, TN, BK>(tl, oa, ob, lds, (int)((rows + 63) / 64), w, lane, [&](auto vs, auto& acc) {
+  tile_sums<BG_FORWARD, TM, TN, BK>(NoGather(), tl, oa, ob, lds, (int)((rows + 63) / 64), w, lane, [&](auto vs, auto& acc) {
     constexpr int VS = decltype(vs)::value;
     float* s_ref = reinterpret_cast<float*>(lds);
     float* s_coef = s_ref + BM;
@@ -562,7 +608,7 @@ __global__ __launch_bounds__(256, 2) void vocab_few_kernel(VocabArgs p) {
     const int64_t c = s_target[threadIdx.x] - n * BN;
     col = c >= 0 && c < BN ? (int)c : -1;
   }
-  tile_sums<BG_FORWARD, 1, TN, BK>(tl, oa, ob, lds, 1, w, lane, [&](auto vs, auto& acc) {
+  tile_sums<BG_FORWARD, 1, TN, BK>(NoGather(), tl, oa, ob, lds, 1, w, lane, [&](auto vs, auto& acc) {
     int* s_col = reinterpret_cast<int*>(lds);
     if (threadIdx.x < 64) s_col[threadIdx.x] = col;
     __syncthreads();
@@ -587,13 +633,12 @@ __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_dh_kernel(Vo
   tl.row_hi = min(count, tl.row_lo + BM);
   tl.K = max((int64_t)0, min(p.per_split, p.width - s0));
   const int64_t rows = tl.row_hi - tl.row_lo;
-  // a split past a short last piece has nothing to sum: no byte of dz either
-  oa.rsrc = bg_rsrc(p.dz + tl.row_lo * p.ld + s0, tl.K > 0 ? rows * p.ld * 2 - s0 * 2 : 0);
-  rows_operand<TM, BK>(oa, rows, (uint32_t)p.ld * 2, w, lane);
+  oa.base = p.dz + tl.row_lo / 64 * p.dz_row + s0 / 64 * p.dz_col;
+  dz_operand<TM, BK, false>(p, oa, rows, w, lane);
   ob.stride = p.k * 2;
   ob.base = reinterpret_cast<const uint8_t*>(p.w + (p.v0 + s0) * p.k + n * BN);
   cols_operand<TN, BK>(ob, p.k - n * BN, w, lane);
-  tile_sums<BG_DGRAD, TM, TN, BK>(tl, oa, ob, lds, (int)((rows + 63) / 64), w, lane, [&](auto vs, auto& acc) {
+  tile_sums<BG_DGRAD, TM, TN, BK>(DzBlocks{{}, p.dz_row, p.dz_col}, tl, oa, ob, lds, (int)((rows + 63) / 64), w, lane, [&](auto vs, auto& acc) {
     float* y = p.sums + split * p.rows * p.k;
     store_tile<decltype(vs)::value, TN, false>(acc, lds, y, p.first ? nullptr : y, p.k, n * BN + 32 * TN * (w & 1), w, lane,
         [&](int r) { return tl.row_lo + r < tl.row_hi ? tl.row_lo + r : (int64_t)-1; });
@@ -615,13 +660,12 @@ __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_dw_kernel(Vo
   tl.row_lo = m * BM;
   tl.row_hi = min(p.width, tl.row_lo + BM);
   tl.K = count;
-  oa.stride = p.ld * 2;
-  oa.base = reinterpret_cast<const uint8_t*>(p.dz + tl.row_lo);
-  cols_operand<TM, BK>(oa, p.ld - tl.row_lo, w, lane);
+  oa.base = p.dz + tl.row_lo / 64 * p.dz_col;
+  dz_operand<TM, BK, true>(p, oa, tl.row_hi - tl.row_lo, w, lane);
   ob.stride = p.k * 2;
   ob.base = reinterpret_cast<const uint8_t*>(p.hc + n * BN);
   cols_operand<TN, BK>(ob, p.k - n * BN, w, lane);
-  tile_sums<BG_WGRAD, TM, TN, BK>(tl, oa, ob, lds, (int)((tl.row_hi - tl.row_lo + 63) / 64), w, lane, [&](auto vs, auto& acc) {
+  tile_sums<BG_WGRAD, TM, TN, BK>(DzBlocks{{}, p.dz_row, p.dz_col}, tl, oa, ob, lds, (int)((tl.row_hi - tl.row_lo + 63) / 64), w, lane, [&](auto vs, auto& acc) {
     constexpr int VS = decltype(vs)::value;
     auto row = [&](int r) { return tl.row_lo + r < tl.row_hi ? p.v0 + tl.row_lo + r : (int64_t)-1; };
     const int64_t col0 = n * BN + 32 * TN * (w & 1);
@@ -734,13 +778,11 @@ static dim3 tile_grid(int64_t tiles) { return dim3((unsigned)(8 * (tiles / 8 + 1
 // a launch has fewer than 2^32 threads
 static bool grid_ok(int64_t tiles) { return tiles < ((int64_t)1 << 24) - 8; }
 
-// Tile of the logits (64 TM rows by 64 TN columns; measured with k = 1032 or
-// 2048, the dz form).  The large tile reads its operands least, and from two
-// rounds of tiles on it is the fastest (8192 rows, vocabulary 131072: see
-// above; 1000 rows: 461 us, 192 x 128 678, 128 x 128 574); where its second row
-// of tiles would be mostly empty, or with few tiles, smaller ones (300 rows:
-// 192 x 128 202 us, 256 x 256 219; 64 rows, vocabulary 32003: 64 x 128 16 us,
-// 256 x 256 19).
+// Tile of the logits (64 TM rows by 64 TN columns; measured in the dz form).  The
+// large tile reads its operands least and is the fastest with a CU's worth of
+// tiles (1000 rows, 131072 x 2048: 480 us, 192 x 128 683, 64 x 128 900); where
+// its second row of tiles would be mostly empty, or with few tiles, smaller ones
+// (301 rows, 32003 x 1032: 192 x 128 38 us, 256 x 256 41, 64 x 128 42).
 struct TileShape {
   int tm, tn;
 };
@@ -764,56 +806,58 @@ static void launch_logits(const VocabArgs& p, hipStream_t str) {
 
 // The pieces of the vocabulary in the backward pass, and tile and splits of dh.
 struct VocabPlan {
-  int64_t width, ld, splits, per_split;
+  int64_t width, splits, per_split;
   TileShape dh, dw;
 };
 static VocabPlan vocab_plan(int64_t rows, int64_t vocab, int64_t k) {
   VocabPlan q;
-  // dz of a piece takes up to 512 MiB: fewer pieces add to dh's sums less often
-  // (8192 rows, vocabulary 131072, k = 2048, 256 x 256 tiles of dh: pieces of
-  // 256 MiB 3609 us, 512 MiB 3448, 1 GiB 3191)
-  int64_t most = ((int64_t)1 << 28) / (rows > 0 ? rows : 1);
-  most = most < 2048 ? 2048 : most;
+  // dz of a piece takes up to 1 GiB: fewer pieces add to dh's sums less often, but
+  // a smaller dz stays in the last cache (8192 rows, 6144 of them with a target,
+  // vocabulary 131072, k = 2048, logits + dh + dw: pieces of 256 MiB 2913 + 3363 +
+  // 2507 us, 512 MiB 3057 + 2805 + 2623, 1 GiB 3163 + 2590 + 2667).  At most 2^21
+  // columns, so that a tile's blocks of dz lie within 2^31 bytes.
+  int64_t most = ((int64_t)1 << 29) / (rows > 0 ? rows : 1);
+  most = most < 2048 ? 2048 : most > (1 << 21) ? (1 << 21) : most;
   const int64_t pieces = vocab > most ? (vocab + most - 1) / most : 1;
   q.width = up((vocab + pieces - 1) / pieces, 256);
   q.width = q.width < 256 ? 256 : q.width;
-  // rows of dz lie 128 bytes off a power of two: its columns would otherwise
-  // fall on few memory channels (writing and reading dz 3 to 6% faster)
-  q.ld = q.width + 64;
   // dh: the sum over the vocabulary is split over blocks, 512 rows of w each at
   // least.  256 x 256 tiles run one a CU in whole rounds; a tile's start and
   // store cost as much as about 1500 rows of w.  Their splits are those of the
-  // shortest rounds, with all, three quarters or half of the rows counted.
+  // shortest rounds, with all or three quarters of the rows counted.
   const int64_t room = q.width / 512 > 0 ? q.width / 512 : 1;
   int64_t best = 0, splits = 1;
   for (int64_t s = 1; s <= 32 && s <= room; ++s) {
     int64_t cost = 0;
-    for (int f = 2; f <= 4; ++f)
+    for (int f = 3; f <= 4; ++f)
       cost += (tiles_of((rows * f + 3) / 4, k, 4, 4) * s + 255) / 256 * (q.width / s + 1500);
     if (s == 1 || cost < best) {
       best = cost;
       splits = s;
     }
   }
-  // They are the fastest where a tile's sum is long (1000 rows, vocabulary
-  // 131072: 508 us, 128 x 256 562); else 128 x 256, two a CU (1000 rows,
-  // vocabulary 32003, k = 1032: 105 us against 143), and 128 x 128 for few rows,
-  // whose sums are split least (301 rows: 38 us against 57).
-  if (rows > 64 && q.width / splits >= 4096) {
+  // Small products leave such tiles too little to sum: two or three smaller ones a
+  // CU start and store past each other.  dh with the join of its splits, 256 x 256
+  // against 128 x 128 (a tenth of the rows without a target): vocabulary 32003, k =
+  // 1032: 100 rows 37 us against 28, 400 rows 60 against 50, 600 rows 72 against
+  // 85; 131072 x 2048: 200 rows 157 against 187, 1000 rows 500 against 547.
+  // dw, whose sum over the rows is short: two 256 x 128 tiles a CU, one of which
+  // stores while the other multiplies (131072 x 2048: 64 rows 131 us, 128 x 128
+  // 151, 400 rows 264 and 316; 32003 x 1032, 100 rows: 39 and 37; 2000 rows: 128,
+  // 256 x 256 149), until the sum is long (8192 rows, 131072 x 2048: 256 x 256 96%
+  // of 256 x 128).
+  const bool small = rows * q.width * k < ((int64_t)1 << 34);
+  if (rows > 64 && !small) {
     q.dh = {4, 4};
   } else {
-    q.dh = rows > 512 ? TileShape{2, 4} : rows > 64 ? TileShape{2, 2} : TileShape{1, 2};
+    q.dh = rows > 64 ? TileShape{2, 2} : TileShape{1, 2};
     const int64_t tiles = tiles_of(rows, k, q.dh.tm, q.dh.tn);
     splits = tiles > 0 ? (512 + tiles - 1) / tiles : 1;
     splits = splits < room ? splits : room;
   }
   q.splits = splits;
   q.per_split = up((q.width + q.splits - 1) / q.splits, 64);
-  // dw: the sum over the rows is short; two 256 x 128 tiles a CU, one of which
-  // stores while the other multiplies, until it is long (8192 rows: 256 x 256
-  // 2752 us, 256 x 128 2858; 1000 rows, vocabulary 131072: 544 and 502; 64 rows,
-  // vocabulary 32003: 256 x 128 38 us, 128 x 128 34)
-  q.dw = rows > 2048 ? TileShape{4, 4} : rows > 64 ? TileShape{4, 2} : TileShape{2, 2};
+  q.dw = rows > 2048 ? TileShape{4, 4} : small ? TileShape{2, 2} : TileShape{4, 2};
   return q;
 }
 
@@ -822,7 +866,7 @@ static int64_t forward_bytes(int64_t rows, int64_t vocab, int64_t k) {
 }
 static int64_t backward_bytes(int64_t rows, int64_t vocab, int64_t k) {
   const VocabPlan q = vocab_plan(rows, vocab, k);
-  return 16 + up(rows, 4) * 4 * 5 + up(rows * k * 2, 16) + up(rows * q.ld * 2, 16) + q.splits * rows * k * 4;
+  return 16 + up(rows, 4) * 4 * 5 + up(rows * k * 2, 16) + up(rows, 64) * q.width * 2 + q.splits * rows * k * 4;
 }
 
 }  // namespace nvfp4
@@ -926,11 +970,12 @@ extern "C" int nvfp4_vocab_loss_backward(const uint16_t* h, const uint16_t* w, c
   p.ref = reinterpret_cast<float*>(p.target + list);
   p.coef = p.ref + list;
   p.hc = reinterpret_cast<uint16_t*>(p.coef + list);
-  p.dz = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(p.hc) + nvfp4::up(rows * k * 2, 16));
-  p.sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.dz) + nvfp4::up(rows * q.ld * 2, 16));
+  p.dz = reinterpret_cast<uint8_t*>(p.hc) + nvfp4::up(rows * k * 2, 16);
+  p.dz_row = q.width * 128;
+  p.dz_col = 8192;
+  p.sums = reinterpret_cast<float*>(p.dz + nvfp4::up(rows, 64) * q.width * 2);
   p.splits = (int)q.splits;
   p.per_split = q.per_split;
-  p.ld = q.ld;
   hipStream_t str = (hipStream_t)stream;
   if (rows > 0) launch_rows<false>(p, str);
   else hipLaunchKernelGGL(nvfp4::vocab_number_kernel, dim3(1), dim3(1024), 0, str, p);  // none: the count
@@ -942,7 +987,6 @@ extern "C" int nvfp4_vocab_loss_backward(const uint16_t* h, const uint16_t* w, c
     if (dh && rows > 0) {
       const dim3 grid = nvfp4::tile_grid(nvfp4::tiles_of(rows, k, q.dh.tm, q.dh.tn) * q.splits);
       if (q.dh.tm == 4) hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<4, 4, 64>), grid, dim3(256), 0, str, p);
-      else if (q.dh.tn == 4) hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<2, 4, 32>), grid, dim3(256), 0, str, p);
       else if (q.dh.tm == 2) hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<2, 2, 64>), grid, dim3(256), 0, str, p);
       else hipLaunchKernelGGL((nvfp4::vocab_dh_kernel<1, 2, 64>), grid, dim3(256), 0, str, p);
     }

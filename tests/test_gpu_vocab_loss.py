@@ -362,3 +362,31 @@ def test_a_table_past_four_gigabytes():
         want = torch.mm(dz[:, rows].t().contiguous(), h.double())
         size = torch.mm(dz[:, rows].abs().t().contiguous(), h.double().abs())
         assert ((got["dw"][rows].double() - want).abs() <= (HALF[BF16] + 1e-3) * size).all()
+
+
+# pieces of the vocabulary: of 2^29 elements of dz, of 2048 columns at least and of 2^21 at most
+@pytest.mark.parametrize("rows,vocab,k", [(40001, 14003, 16), (270001, 2500, 8), (300, 2 ** 21 + 77, 8), (3, 4500001, 8)])
+def test_pieces_of_the_vocabulary(rows, vocab, k):
+    h, w, t, d = inputs(rows, vocab, k, std=2.0)
+    t[0] = vocab - 1
+    got = nv.nvfp4_vocab_loss(h, w, t)
+    check_loss(got, exact_loss(h, w, t, 1.0))
+    g = nv.nvfp4_vocab_loss_backward(h, w, t, got["lse"], d)
+    for name, (want, bound) in exact_grads(h, w, t, got["lse"], d, 1.0).items():
+        close(g[name], want, bound, name)
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rows", [5, 70, 333])
+def test_an_infinite_row_of_the_table(rows):
+    """A table row that every logit of is -infinity has probability 0 and a zero
+    gradient, whatever lies past the last row with a target."""
+    h, w, t, d = inputs(rows, 1000, 64, ignored=0.0)
+    h[:, 0] = h[:, 0].abs() + 1
+    w[5, 0] = -float("inf")
+    t[t == 5] = 6
+    t[-2:] = -1
+    got = nv.nvfp4_vocab_loss(h, w, t)
+    assert torch.isfinite(got["loss"]).all()
+    dw = nv.nvfp4_vocab_loss_backward(h, w, t, got["lse"], d, want_dh=False)["dw"]
+    assert (dw[5] == 0).all() and torch.isfinite(dw).all()
