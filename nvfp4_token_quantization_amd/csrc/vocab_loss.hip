@@ -34,14 +34,14 @@
 // 3.3 TFLOP a product; the library's bf16 products of these sizes take 2428 to
 // 2654 us for the logits, 2570 to 2876 for dz w, 2892 to 3134 for dz^T h):
 //   forward   2830 us: rows 22, logits 2790, join 12
-//   backward  8440 us: rows 24, dz 3060 to 3160, dh 2590, dw 2660, join 88
+//   backward  8440 us: rows 24, dz 3060 to 3160, dh 2590, dw 2660, join 77
 // bound by the matrix cores: a 256 x 256 tile takes 1.4 us per 64 of k, 1550
 // TFLOP/s were it all, and 10 us to start and leave its sums, 16 to leave dz.
 // Tried and slower: persistent blocks that load the next tile's first stages
 // under the epilogue (3030 us of logits), BK = 32 (2836), streaming stores of dz
 // (3% of the logits).
 //   64 rows, 131072 x 2560: 129 us, the table read at 5.2 TB/s
-//   301 rows, 32003 x 1032, backward: 130 us, dw 45, dz 38, dh 32
+//   301 rows, 32003 x 1032, backward: 126 us, dw 42, dz 40, dh 33
 #include <type_traits>
 
 #include "bf16_tile.h"
@@ -393,8 +393,12 @@ __device__ __forceinline__ void tile_dz(const VocabArgs& p, const Acc<VS, TN>& a
 // Store of a tile, 16 rows of a wave at a time through LDS (2 TN KiB a wave,
 // columns XOR-swizzled by row so that the four lane groups write other banks):
 // 16 bytes a lane, fp32 or bf16, with `add` (may be y itself) added.  row_of: the
-// output row of a row of the tile, -1: none; N columns a row.
-template <int VS, int TN, bool BF, class Row>
+// output row of a row of the tile, -1: none; N columns a row.  STREAM past the
+// caches, so that w stays in them (64 rows, 131072 x 2048: the logits 112 us, else
+// 175), but for bf16 rows that are no whole lines: a piece of a line waits in the
+// L2 for the next tile's (32003 x 1032, 64 rows, dw: 25 us, streamed 35; fp32
+// pieces are twice as long and gain nothing).
+template <int VS, int TN, bool BF, bool STREAM, class Row>
 __device__ __forceinline__ void store_tile(const Acc<VS, TN>& acc, uint8_t* lds, void* y, const void* add, int64_t N,
                                            int64_t col0, int w, int lane, Row&& row_of) {
   constexpr int CPP = BF ? 8 : 4, LPR = 32 * TN / CPP, U = 16 * LPR / 64, ES = BF ? 2 : 4;
@@ -439,7 +443,10 @@ __device__ __forceinline__ void store_tile(const Acc<VS, TN>& acc, uint8_t* lds,
         if (add) x += __builtin_bit_cast(f32x4, av[u]);
         o = __builtin_bit_cast(u32x4, x);
       }
-      if (at[u] >= 0) __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(static_cast<uint8_t*>(y) + at[u]));
+      if (at[u] < 0) continue;
+      u32x4* to = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(y) + at[u]);
+      if (STREAM) __builtin_nontemporal_store(o, to);
+      else *to = o;
     }
     wave_lds_sync();
   }
@@ -640,7 +647,7 @@ __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_dh_kernel(Vo
   cols_operand<TN, BK>(ob, p.k - n * BN, w, lane);
   tile_sums<BG_DGRAD, TM, TN, BK>(DzBlocks{{}, p.dz_row, p.dz_col}, tl, oa, ob, lds, (int)((rows + 63) / 64), w, lane, [&](auto vs, auto& acc) {
     float* y = p.sums + split * p.rows * p.k;
-    store_tile<decltype(vs)::value, TN, false>(acc, lds, y, p.first ? nullptr : y, p.k, n * BN + 32 * TN * (w & 1), w, lane,
+    store_tile<decltype(vs)::value, TN, false, true>(acc, lds, y, p.first ? nullptr : y, p.k, n * BN + 32 * TN * (w & 1), w, lane,
         [&](int r) { return tl.row_lo + r < tl.row_hi ? tl.row_lo + r : (int64_t)-1; });
   });
 }
@@ -669,8 +676,9 @@ __global__ __launch_bounds__(256, (bg_blocks<TM, TN>())) void vocab_dw_kernel(Vo
     constexpr int VS = decltype(vs)::value;
     auto row = [&](int r) { return tl.row_lo + r < tl.row_hi ? p.v0 + tl.row_lo + r : (int64_t)-1; };
     const int64_t col0 = n * BN + 32 * TN * (w & 1);
-    if (p.dw_bf) store_tile<VS, TN, true>(acc, lds, p.dw, p.add, p.k, col0, w, lane, row);
-    else store_tile<VS, TN, false>(acc, lds, p.dw, p.add, p.k, col0, w, lane, row);
+    if (p.dw_bf && p.k % 64) store_tile<VS, TN, true, false>(acc, lds, p.dw, p.add, p.k, col0, w, lane, row);
+    else if (p.dw_bf) store_tile<VS, TN, true, true>(acc, lds, p.dw, p.add, p.k, col0, w, lane, row);
+    else store_tile<VS, TN, false, true>(acc, lds, p.dw, p.add, p.k, col0, w, lane, row);
   });
 }
 
@@ -739,11 +747,12 @@ __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabArgs p) {
       for (int s0 = g; s0 < p.splits; s0 += 32) {  // four in flight
         f32x4 u[4], v[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const f32x4* q = reinterpret_cast<const f32x4*>(p.sums + ((int64_t)min(s0 + 8 * s, p.splits - 1) * p.rows + at) * p.k + e);
-          u[s] = __builtin_nontemporal_load(q);
-          v[s] = __builtin_nontemporal_load(q + 1);
-        }
+        for (int s = 0; s < 4; ++s)
+          if (s0 + 8 * s < p.splits) {
+            const f32x4* q = reinterpret_cast<const f32x4*>(p.sums + ((int64_t)(s0 + 8 * s) * p.rows + at) * p.k + e);
+            u[s] = __builtin_nontemporal_load(q);
+            v[s] = __builtin_nontemporal_load(q + 1);
+          }
 #pragma unroll
         for (int s = 0; s < 4; ++s)
           if (s0 + 8 * s < p.splits) {
@@ -1000,7 +1009,7 @@ extern "C" int nvfp4_vocab_loss_backward(const uint16_t* h, const uint16_t* w, c
   if (dh && rows > 0) {
     const int64_t blocks = (rows * (k / 8) + 31) / 32;
     if (vocab == 0) p.splits = 0;
-    hipLaunchKernelGGL(nvfp4::vocab_dh_join_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, str, p);
+    hipLaunchKernelGGL(nvfp4::vocab_dh_join_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, str, p);
   }
   return nvfp4host::launch_status();
 }
